@@ -38,7 +38,7 @@
 extern "C" {
 #endif
 
-#define MOE_ABI_VERSION 5
+#define MOE_ABI_VERSION 6
 
 typedef enum {
     MOE_OK = 0,
@@ -54,7 +54,12 @@ enum { MOE_W_MXFP4 = 0, MOE_W_FP8_E4M3_B128 = 1 };
  * MOE_ACT_MXFP4: x and h are OCP-MX-quantised to MXFP4 per 32-block and the products run on
  *                the block-scaled FP4 matrix cores (MXFP4 weights only). */
 enum { MOE_ACT_FLOAT = 0, MOE_ACT_MXFP4 = 1 };
-enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1 };
+/* MOE_DT_MXFP8: OCP MXFP8 codes with their E8M0 scales beside them (moe_mxfp8_quantize). */
+enum { MOE_DT_BF16 = 0, MOE_DT_F32 = 1, MOE_DT_MXFP8 = 2 };
+/* Activations of the dense layers: z; z s(z) (s the logistic function); z Phi(z) (Phi the normal
+ * distribution function); 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); max(z, 0), whose
+ * derivative at 0 is 0. */
+enum { MOE_FN_NONE = 0, MOE_FN_SILU = 1, MOE_FN_GELU = 2, MOE_FN_GELU_TANH = 3, MOE_FN_RELU = 4 };
 
 typedef void *moe_stream; /* hipStream_t */
 
@@ -371,6 +376,98 @@ moe_status moe_dequant_bf16(int32_t n, int32_t kdim, const uint8_t *codes, const
  */
 moe_status moe_mx_quantize(int32_t rows, int32_t cols, const void *x, int32_t x_dtype,
                            uint8_t *codes, uint8_t *scales, moe_stream stream);
+
+/*
+ * Dense bf16 layers: the feed-forward block that runs on every token beside the routed experts
+ * (the dense layers and a bf16 shared expert: rabbit README, design section and architecture
+ * table), and its gradients.  For all of them: weights bf16, row-major [n][kdim]; biases float32;
+ * sums, activations and bias gradients in float32; every matrix has fewer than 2^31 elements;
+ * tensors 16-byte aligned; kdim, d_model and d_ff multiples of 8.  A NaN or infinity reaches
+ * the outputs whose sums it takes part in, and no others.  Results depend on the arguments alone:
+ * the same call gives the same bits (sums have a fixed order; no atomics).  The workspace is
+ * 16-byte aligned; calls that may run at the same time (other streams, other captured graphs)
+ * need one each.
+ *
+ * moe_dense_linear -- y = f(x W^T + bias) + residual.
+ *   x [T][kdim] of x_dtype (bf16 or float32), W [n][kdim], bias [n] or NULL, residual [T][n] of
+ *   y_dtype or NULL (may be y itself), y [T][n] of y_dtype (bf16 or float32).  Any n >= 1.
+ *   float32 x is used exactly: as float32 for T <= 8, else as three bf16 terms whose sum it is.
+ *   Ranges: up to 8 tokens read the weights once on the vector ALU and need no workspace; more run
+ *   on the matrix cores, few tiles with the sum split over workgroups.
+ * moe_dense_linear_backward -- with z = x W^T + bias and dz = dy f'(z):
+ *   dx = dz W [T][kdim] bf16, dw = dz^T x [n][kdim] bf16, dbias = sum_t dz float32 [n].
+ *   x is bf16, or MXFP8 codes with x_scales (x_dtype MOE_DT_MXFP8, kdim a multiple of 32): the
+ *   8-bit checkpoint stands for x everywhere, also in z.  dy bf16 [T][n].  z is recomputed when fn is not
+ *   MOE_FN_NONE; dz is rounded to bf16 for the two products (the matrix cores' operand type) and not for
+ *   dbias.  Any of dx, dw, dbias may be NULL (not wanted), not all.  The residual's gradient is dy.
+ *   x may be NULL when fn is MOE_FN_NONE and dw is NULL; w when fn is MOE_FN_NONE and dx is NULL.
+ *   bias is read only when fn is not MOE_FN_NONE.  y_dtype is ignored.
+ *   With T == 0 dw and dbias are written as zeros.
+ */
+typedef struct {
+    int32_t T, n, kdim;
+    int32_t fn;           /* MOE_FN_*                                   */
+    int32_t x_dtype;      /* MOE_DT_*: type of x                        */
+    int32_t y_dtype;      /* MOE_DT_BF16 or MOE_DT_F32: type of y       */
+} moe_linear_desc;
+moe_status moe_dense_linear(const moe_linear_desc *desc, const void *x, const void *w, const float *bias,
+                            const void *residual, void *y, void *ws, size_t ws_bytes, moe_stream stream);
+size_t moe_dense_linear_workspace(const moe_linear_desc *desc);
+moe_status moe_dense_linear_backward(const moe_linear_desc *desc, const void *dy, const void *x,
+                                     const uint8_t *x_scales, const void *w, const float *bias, void *dx, void *dw,
+                                     float *dbias, void *ws, size_t ws_bytes, moe_stream stream);
+size_t moe_dense_linear_backward_workspace(const moe_linear_desc *desc);
+
+/*
+ * moe_dense_gateup -- the gated projections of a dense feed-forward block, both products, the
+ * activation and the product in one kernel:
+ *   g = x w_gate^T + b_gate, u = x w_up^T + b_up, h = f(g) * u.
+ *   x bf16 [T][d_model]; w_gate, w_up [d_ff][d_model]; b_gate, b_up [d_ff] or NULL;
+ *   h [T][d_ff] of h_dtype (bf16 or float32); pre: bf16 [2][T][d_ff] (g, then u, rounded) or NULL.
+ *   With moe_dense_linear as its down projection this is a whole SwiGLU / GEGLU / ReGLU block.
+ * moe_dense_gateup_backward -- from dh [T][d_ff] bf16:
+ *   dg = dh u f'(g), du = dh f(g);  dx = dg w_gate + du w_up [T][d_model] bf16;
+ *   dw_gate = dg^T x, dw_up = du^T x [d_ff][d_model] bf16; db_gate, db_up: column sums, float32.
+ *   pre == NULL: g and u are recomputed from x in the product kernel, which forms dg and du in
+ *   its epilogue; pre given: they are read (b_gate and b_up are not).  x is bf16 or the MXFP8
+ *   checkpoint with x_scales (x_dtype, d_model a multiple of 32); it may be NULL when pre is given and
+ *   dw_gate is NULL.  h: bf16 [T][d_ff] or NULL, recomputed for the down projection's weight gradient.
+ *   dg and du are rounded to bf16 for the products and not for the bias gradients.  dw_gate and
+ *   dw_up come together or not at all, as do db_gate and db_up; dx, dw_*, db_* and h may be NULL, not all.
+ *   With T == 0 the weight and bias gradients are written as zeros.
+ */
+typedef struct {
+    int32_t T, d_model, d_ff;
+    int32_t fn;           /* MOE_FN_*                                   */
+    int32_t x_dtype;      /* MOE_DT_BF16, or MOE_DT_MXFP8 (backward)    */
+    int32_t h_dtype;      /* MOE_DT_BF16 or MOE_DT_F32 (forward)        */
+} moe_gateup_desc;
+moe_status moe_dense_gateup(const moe_gateup_desc *desc, const void *x, const void *w_gate, const void *w_up,
+                            const float *b_gate, const float *b_up, void *h, void *pre, void *ws, size_t ws_bytes,
+                            moe_stream stream);
+size_t moe_dense_gateup_workspace(const moe_gateup_desc *desc);
+moe_status moe_dense_gateup_backward(const moe_gateup_desc *desc, const void *dh, const void *x,
+                                     const uint8_t *x_scales, const void *w_gate, const void *w_up,
+                                     const float *b_gate, const float *b_up, const void *pre, void *dx,
+                                     void *dw_gate, void *dw_up, float *db_gate, float *db_up, void *h, void *ws,
+                                     size_t ws_bytes, moe_stream stream);
+size_t moe_dense_gateup_backward_workspace(const moe_gateup_desc *desc);
+
+/*
+ * moe_mxfp8_quantize -- OCP MX conversion of rows [rows][cols] (bf16 or float32, cols a multiple of
+ * 32) to MXFP8: per 32-block scale byte X+127 with X = floor(log2 amax) - 8 clamped to [-127,127]
+ * (byte 0 for an all-zero block, 0xFF and zero codes for a block holding NaN or Inf); codes =
+ * nearest E4M3 of v/2^X, ties to even, saturating at 448, sign kept.  codes uint8 [rows][cols],
+ * scales uint8 [rows][cols/32].  An activation kept this way for the backward pass takes 33/64 of
+ * its bf16 bytes; both *_backward calls above read it directly.
+ * moe_mxfp8_dequant -- E4M3(code) * 2^(scale-127) to bf16 (exact but for bf16's subnormals) or
+ * float32.  values and codes 16-byte aligned.
+ * (The element and scale formats: rabbit README, architecture table, OCP MXFP4 and FP8 E4M3.)
+ */
+moe_status moe_mxfp8_quantize(int32_t rows, int32_t cols, const void *x, int32_t x_dtype, uint8_t *codes,
+                              uint8_t *scales, moe_stream stream);
+moe_status moe_mxfp8_dequant(int32_t rows, int32_t cols, const uint8_t *codes, const uint8_t *scales, void *out,
+                             int32_t out_dtype, moe_stream stream);
 
 /* Text of the last error on the calling thread; valid until the next call on it. */
 const char *moe_last_error(void);

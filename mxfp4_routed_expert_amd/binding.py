@@ -7,7 +7,9 @@ module raises: there is no fallback.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -21,6 +23,8 @@ SCORE = {"softmax": 0, "sigmoid": 1}
 WFMT = {"mxfp4": 0, "fp8b128": 1}
 ACT = {"float": 0, "mxfp4": 1}
 DT = {torch.bfloat16: 0, torch.float32: 1}
+DT_MXFP8 = 2
+ACT_FN = {"none": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3, "relu": 4}
 
 
 class MoeError(RuntimeError):
@@ -49,6 +53,14 @@ class RouteDesc(ctypes.Structure):
 class ExpertWeightsC(ctypes.Structure):
     _fields_ = [("format", _i32), ("num_experts", _i32), ("d_model", _i32), ("d_ff", _i32),
                 ("gate", _p), ("up", _p), ("down", _p), ("gate_s", _p), ("up_s", _p), ("down_s", _p)]
+
+
+class LinearDesc(ctypes.Structure):
+    _fields_ = [("T", _i32), ("n", _i32), ("kdim", _i32), ("fn", _i32), ("x_dtype", _i32), ("y_dtype", _i32)]
+
+
+class GateupDesc(ctypes.Structure):
+    _fields_ = [("T", _i32), ("d_model", _i32), ("d_ff", _i32), ("fn", _i32), ("x_dtype", _i32), ("h_dtype", _i32)]
 
 
 def _sig(name, res, *args):
@@ -87,6 +99,17 @@ _sig("moe_dense_bf16", _i32, _i32, _i32, _i32, _p, _i32, _p, _p, _p, _p)
 _sig("moe_dequant_bf16", _i32, _i32, _i32, _p, _p, _p, _p)
 _sig("moe_dequant", _i32, _i32, _i32, _i32, _p, _p, _p, _p)
 _sig("moe_mx_quantize", _i32, _i32, _i32, _p, _i32, _p, _p, _p)
+_sig("moe_dense_linear", _i32, ctypes.POINTER(LinearDesc), _p, _p, _p, _p, _p, _p, _sz, _p)
+_sig("moe_dense_linear_workspace", _sz, ctypes.POINTER(LinearDesc))
+_sig("moe_dense_linear_backward", _i32, ctypes.POINTER(LinearDesc), _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p)
+_sig("moe_dense_linear_backward_workspace", _sz, ctypes.POINTER(LinearDesc))
+_sig("moe_dense_gateup", _i32, ctypes.POINTER(GateupDesc), _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p)
+_sig("moe_dense_gateup_workspace", _sz, ctypes.POINTER(GateupDesc))
+_sig("moe_dense_gateup_backward", _i32, ctypes.POINTER(GateupDesc), _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p,
+     _p, _p, _sz, _p)
+_sig("moe_dense_gateup_backward_workspace", _sz, ctypes.POINTER(GateupDesc))
+_sig("moe_mxfp8_quantize", _i32, _i32, _i32, _p, _i32, _p, _p, _p)
+_sig("moe_mxfp8_dequant", _i32, _i32, _i32, _p, _p, _p, _i32, _p)
 
 EXPORTS = ["moe_route", "moe_route_workspace", "moe_permute", "moe_permute_workspace", "moe_route_permute",
            "moe_route_permute_noalloc",
@@ -94,7 +117,10 @@ EXPORTS = ["moe_route", "moe_route_workspace", "moe_permute", "moe_permute_works
            "moe_expert_down_combine", "moe_decode_step", "moe_decode_step_sync_bytes",
            "moe_expert_ffn_workspace", "moe_expert_gateup", "moe_expert_gateup_workspace", "moe_expert_down",
            "moe_combine", "moe_dense_bf16", "moe_dequant", "moe_dequant_bf16", "moe_mx_quantize", "moe_last_error",
-           "moe_abi_version"]
+           "moe_abi_version", "moe_dense_linear", "moe_dense_linear_workspace", "moe_dense_linear_backward",
+           "moe_dense_linear_backward_workspace", "moe_dense_gateup", "moe_dense_gateup_workspace",
+           "moe_dense_gateup_backward", "moe_dense_gateup_backward_workspace", "moe_mxfp8_quantize",
+           "moe_mxfp8_dequant"]
 
 
 def last_error() -> str:
@@ -536,3 +562,227 @@ def moe_mx_quantize(x):
     scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
     check(lib.moe_mx_quantize(rows, cols, _ptr(x), DT[x.dtype], _ptr(codes), _ptr(scales), _stream()))
     return codes, scales
+
+
+# ------------------------------------------------------------------ dense bf16 layers
+
+@contextlib.contextmanager
+def _switched(index):
+    with torch.cuda.device(index):
+        yield
+
+
+def _on(x):
+    """The device of x as the current device for a call (its current stream is then the one used)."""
+    i = x.device.index
+    return _switched(i) if i != torch.cuda.current_device() else _HERE_ALREADY
+
+
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _operands(dev, *items):
+    """items: (tensor or None, dtype or tuple of dtypes, name, shape).  All on `dev`, contiguous, 16-byte aligned."""
+    for t, dtype, name, shape in items:
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if isinstance(dtype, tuple):
+            if t.dtype not in dtype:
+                raise TypeError(f"{name} must be one of {dtype} (got {t.dtype})")
+            dtype = None
+        _need(t, dtype, name, shape)
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _matrix(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions (got shape {tuple(t.shape)})")
+    return t.shape
+
+
+def _act_fn(name):
+    if name not in ACT_FN:
+        raise ValueError(f"act_fn must be one of {sorted(ACT_FN)} (got {name!r})")
+    return ACT_FN[name]
+
+
+@functools.lru_cache(maxsize=4096)
+def _dense_plan(kind, *sizes):
+    """(descriptor, workspace bytes) of a dense call: a function of its sizes and types alone."""
+    d = (LinearDesc if kind.startswith("linear") else GateupDesc)(*sizes)
+    return d, getattr(lib, f"moe_dense_{kind}_workspace")(ctypes.byref(d))
+
+
+def moe_dense_linear_workspace(T, n, kdim, act_fn="none", x_dtype=torch.bfloat16, out_dtype=torch.bfloat16):
+    return _dense_plan("linear", T, n, kdim, _act_fn(act_fn), DT[x_dtype], DT[out_dtype])[1]
+
+
+def moe_dense_linear_backward_workspace(T, n, kdim, act_fn="none", mxfp8=False):
+    return _dense_plan("linear_backward", T, n, kdim, _act_fn(act_fn), DT_MXFP8 if mxfp8 else 0, 0)[1]
+
+
+def moe_dense_gateup_workspace(T, d_model, d_ff, act_fn="silu", out_dtype=torch.bfloat16):
+    return _dense_plan("gateup", T, d_model, d_ff, _act_fn(act_fn), 0, DT[out_dtype])[1]
+
+
+def moe_dense_gateup_backward_workspace(T, d_model, d_ff, act_fn="silu", mxfp8=False):
+    return _dense_plan("gateup_backward", T, d_model, d_ff, _act_fn(act_fn), DT_MXFP8 if mxfp8 else 0, 0)[1]
+
+
+def _ws_for(ws, need, dev):
+    if need == 0:
+        return None, 0
+    if ws is None:
+        ws = _workspace(need, dev)
+    else:
+        _operands(dev, (ws, torch.uint8, "ws", None))
+    return ws, ws.numel()
+
+
+def moe_dense_linear(x, w, bias=None, act_fn="none", residual=None, out=None, out_dtype=None, ws=None):
+    """y = act_fn(x w^T + bias) + residual.  x [T][kdim] bf16 or float32, w bf16 [n][kdim], bias float32 [n],
+    residual [T][n] of y's type; y [T][n] of out_dtype (x's type when None), bf16 or float32."""
+    T, kdim = _matrix(x, "x")
+    n = _matrix(w, "w")[0]
+    dt = out.dtype if out is not None else (out_dtype or x.dtype)
+    if dt not in DT:
+        raise TypeError(f"y must be bfloat16 or float32 (got {dt})")
+    dev = x.device
+    _operands(dev, (x, tuple(DT), "x", None), (w, torch.bfloat16, "w", (n, kdim)), (bias, torch.float32, "bias", (n,)),
+              (residual, dt, "residual", (T, n)), (out, dt, "out", (T, n)))
+    d, need = _dense_plan("linear", T, n, kdim, _act_fn(act_fn), DT[x.dtype], DT[dt])
+    with _on(x):
+        y = out if out is not None else torch.empty((T, n), dtype=dt, device=dev)
+        ws, nws = _ws_for(ws, need, dev)
+        check(lib.moe_dense_linear(ctypes.byref(d), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(ws), nws,
+                                   _stream()))
+    return y
+
+
+def _wanted(want, names):
+    unknown = set(want) - set(names)
+    if unknown or not want:
+        raise ValueError(f"want must name some of {names} (got {tuple(want)})")
+    return [n in want for n in names]
+
+
+def _saved_input(x, x_scales, T, width, what):
+    """(x_dtype, operand rows) of an input kept as bf16 or as MXFP8 codes with their scales."""
+    mx = x_scales is not None
+    return (DT_MXFP8 if mx else 0), ((x, torch.uint8 if mx else torch.bfloat16, what, (T, width)),
+                                     (x_scales, torch.uint8, "x_scales", (T, width // 32)))
+
+
+def moe_dense_linear_backward(dy, x, w, bias=None, act_fn="none", x_scales=None, want=("dx", "dw", "dbias"), out=None,
+                              ws=None):
+    """Gradients of moe_dense_linear at dy (bf16 [T][n]): (dx bf16 [T][kdim], dw bf16 [n][kdim], dbias float32 [n]), None
+    for what `want` does not name.  x: bf16, or the codes of moe_mxfp8_quantize with their x_scales.
+    out: the three results' tensors (None where not wanted)."""
+    T, n = _matrix(dy, "dy")
+    kdim = _matrix(w, "w")[1]
+    fx, fw, fb = _wanted(want, ("dx", "dw", "dbias"))
+    xdt, xitems = _saved_input(x, x_scales, T, kdim, "x")
+    dev = dy.device
+    ox, ow, ob = out if out is not None else (None, None, None)
+    bf = torch.bfloat16
+    _operands(dev, (dy, bf, "dy", None), *xitems, (w, bf, "w", (n, kdim)), (bias, torch.float32, "bias", (n,)),
+              (ox, bf, "dx", (T, kdim)), (ow, bf, "dw", (n, kdim)), (ob, torch.float32, "dbias", (n,)))
+    d, need = _dense_plan("linear_backward", T, n, kdim, _act_fn(act_fn), xdt, 0)
+    with _on(dy):
+        e = lambda o, on, shape, dt: None if not on else (o if o is not None else torch.empty(shape, dtype=dt, device=dev))
+        dx, dw, db = e(ox, fx, (T, kdim), bf), e(ow, fw, (n, kdim), bf), e(ob, fb, (n,), torch.float32)
+        ws, nws = _ws_for(ws, need, dev)
+        check(lib.moe_dense_linear_backward(ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(x_scales), _ptr(w), _ptr(bias),
+                                            _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nws, _stream()))
+    return dx, dw, db
+
+
+def moe_dense_gateup(x, w_gate, w_up, b_gate=None, b_up=None, act_fn="silu", out=None, out_dtype=None, want_pre=False,
+                     pre=None, ws=None):
+    """h = act_fn(x w_gate^T + b_gate) * (x w_up^T + b_up), both products in one kernel.  x bf16 [T][d_model], weights
+    bf16 [d_ff][d_model], biases float32 [d_ff].  Returns (h [T][d_ff] of out_dtype (bf16 when None), the bf16
+    pre-activations [2][T][d_ff] for the backward call, or None)."""
+    T, dm = _matrix(x, "x")
+    f = _matrix(w_gate, "w_gate")[0]
+    bf = torch.bfloat16
+    dt = out.dtype if out is not None else (out_dtype or bf)
+    if dt not in DT:
+        raise TypeError(f"h must be bfloat16 or float32 (got {dt})")
+    dev = x.device
+    _operands(dev, (x, bf, "x", None), (w_gate, bf, "w_gate", (f, dm)), (w_up, bf, "w_up", (f, dm)),
+              (b_gate, torch.float32, "b_gate", (f,)), (b_up, torch.float32, "b_up", (f,)), (out, dt, "out", (T, f)),
+              (pre, bf, "pre", (2, T, f)))
+    d, need = _dense_plan("gateup", T, dm, f, _act_fn(act_fn), 0, DT[dt])
+    with _on(x):
+        h = out if out is not None else torch.empty((T, f), dtype=dt, device=dev)
+        if pre is None and want_pre:
+            pre = torch.empty((2, T, f), dtype=bf, device=dev)
+        ws, nws = _ws_for(ws, need, dev)
+        check(lib.moe_dense_gateup(ctypes.byref(d), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(b_gate), _ptr(b_up), _ptr(h),
+                                   _ptr(pre), _ptr(ws), nws, _stream()))
+    return h, pre
+
+
+def moe_dense_gateup_backward(dh, x, w_gate, w_up, b_gate=None, b_up=None, act_fn="silu", x_scales=None, pre=None,
+                              want=("dx", "dw", "db"), want_h=False, out=None, ws=None):
+    """Gradients of moe_dense_gateup at dh (bf16 [T][d_ff]): (dx, dw_gate, dw_up, db_gate, db_up, h), None for what was
+    not asked for; h (bf16) is the forward result again, for the down projection's weight gradient.  x: bf16, or MXFP8
+    codes with x_scales; pre: the forward call's pre-activations (recomputed from x when None).  out: the six results'
+    tensors."""
+    T, f = _matrix(dh, "dh")
+    dm = _matrix(w_gate, "w_gate")[1]
+    fx, fw, fb = _wanted(want, ("dx", "dw", "db")) if want or not want_h else (False, False, False)
+    xdt, xitems = _saved_input(x, x_scales, T, dm, "x")
+    dev = dh.device
+    bf, f32 = torch.bfloat16, torch.float32
+    o = out if out is not None else (None,) * 6
+    names = ("dx", "dw_gate", "dw_up", "db_gate", "db_up", "h")
+    shapes = ((T, dm), (f, dm), (f, dm), (f,), (f,), (T, f))
+    types = (bf, bf, bf, f32, f32, bf)
+    _operands(dev, (dh, bf, "dh", None), *xitems, (w_gate, bf, "w_gate", (f, dm)), (w_up, bf, "w_up", (f, dm)),
+              (b_gate, f32, "b_gate", (f,)), (b_up, f32, "b_up", (f,)), (pre, bf, "pre", (2, T, f)),
+              *((t, dt, nm, sh) for t, dt, nm, sh in zip(o, types, names, shapes)))
+    d, need = _dense_plan("gateup_backward", T, dm, f, _act_fn(act_fn), xdt, 0)
+    with _on(dh):
+        r = [None if not on else (t if t is not None else torch.empty(sh, dtype=dt, device=dev))
+             for t, dt, sh, on in zip(o, types, shapes, (fx, fw, fw, fb, fb, want_h))]
+        ws, nws = _ws_for(ws, need, dev)
+        check(lib.moe_dense_gateup_backward(ctypes.byref(d), _ptr(dh), _ptr(x), _ptr(x_scales), _ptr(w_gate), _ptr(w_up),
+                                            _ptr(b_gate), _ptr(b_up), _ptr(pre), *map(_ptr, r), _ptr(ws), nws, _stream()))
+    return tuple(r)
+
+
+def moe_mxfp8_quantize(x, out=None):
+    """Rows of x (bf16 or float32, a multiple of 32 wide) as OCP MXFP8: (codes uint8 [rows][cols], E8M0 scales uint8
+    [rows][cols/32]).  out: the two tensors."""
+    rows, cols = _matrix(x, "x")
+    dev = x.device
+    codes, scales = out if out is not None else (None, None)
+    _operands(dev, (x, tuple(DT), "x", None), (codes, torch.uint8, "codes", (rows, cols)),
+              (scales, torch.uint8, "scales", (rows, cols // 32)))
+    with _on(x):
+        if out is None:
+            codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+            scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+        check(lib.moe_mxfp8_quantize(rows, cols, _ptr(x), DT[x.dtype], _ptr(codes), _ptr(scales), _stream()))
+    return codes, scales
+
+
+def moe_mxfp8_dequant(codes, scales, out=None, out_dtype=torch.bfloat16):
+    """The values of moe_mxfp8_quantize's codes and scales, bf16 or float32."""
+    rows, cols = _matrix(codes, "codes")
+    dev = codes.device
+    dt = out.dtype if out is not None else out_dtype
+    if dt not in DT:
+        raise TypeError(f"values must be bfloat16 or float32 (got {dt})")
+    _operands(dev, (codes, torch.uint8, "codes", None), (scales, torch.uint8, "scales", (rows, cols // 32)),
+              (out, dt, "out", (rows, cols)))
+    with _on(codes):
+        o = out if out is not None else torch.empty((rows, cols), dtype=dt, device=dev)
+        check(lib.moe_mxfp8_dequant(rows, cols, _ptr(codes), _ptr(scales), _ptr(o), DT[dt], _stream()))
+    return o

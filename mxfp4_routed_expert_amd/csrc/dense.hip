@@ -1,0 +1,488 @@
+// Entry points of the dense bf16 layers: argument checks, plans, workspaces and launches.
+#include "dense.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kCUs = 256;            // the plan is a pure function of the sizes (workspace queries run anywhere)
+
+struct Tile {
+    int br, bc, wr, per_cu;
+    double step, tile;               // cost of a 64-value step of a full CU, and of a tile's start and end, in us
+};
+constexpr Tile kTiles[3] = {{256, 256, 2, 1, 1.15, 6.0}, {128, 128, 2, 2, 0.75, 4.0}, {64, 128, 1, 3, 0.75, 3.5}};
+constexpr int kMaxSplit = 16;
+
+}  // namespace
+
+// The tile shape and split with the least estimated time: rounds of workgroups over the CUs times
+// their steps, plus the traffic of the partial results and the launch that sums them.
+DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg) {
+    DensePlan best = {};
+    double best_t = 1e30;
+    const int steps = (K + 63) / 64 * nseg;
+    const int mats = pair ? 2 : 1;
+    for (int cfg = 0; cfg < (form == kFormTN ? 2 : 3); ++cfg) {
+        const Tile &t = kTiles[cfg];
+        const int tr = (R + t.br - 1) / t.br, tc = (C * mats + t.bc - 1) / t.bc;
+        const int64_t tiles = (int64_t)tr * tc;
+        for (int split = 1; split <= kMaxSplit; ++split) {
+            if (split > 1 && (split * 4 > steps || R > 65536 || tiles * split > 4 * kCUs)) break;
+            const int64_t wgs = tiles * split;
+            const int64_t slots = (int64_t)kCUs * t.per_cu;
+            const int64_t rounds = (wgs + slots - 1) / slots;
+            // a last round that fills fewer workgroups per CU runs its steps faster
+            const int64_t last = (wgs - (rounds - 1) * slots + kCUs - 1) / kCUs;
+            const double load = (double)(rounds - 1) + (0.35 + 0.65 * (double)last / t.per_cu);
+            double us = load * (((steps + split - 1) / split) * t.step + t.tile);
+            if (split > 1) us += 3.0 + (double)R * C * mats * 4.0 * split * 2.0 / 4.0e6;
+            if (us < best_t) {
+                best_t = us;
+                best = DensePlan{cfg, split, tr, tc, steps,
+                                 split > 1 ? (R + kFinishRows - 1) / kFinishRows : tr * t.wr};
+            }
+        }
+    }
+    return best;
+}
+
+size_t dense_plan_bytes(const DensePlan &pl, bool pair, int R, int C) {
+    if (pl.split == 1) return 0;
+    return (size_t)pl.split * (pair ? 2 : 1) * R * ((C + 3) & ~3) * sizeof(float);
+}
+
+namespace {
+
+// Consecutive 256-byte-aligned pieces of a workspace; with a NULL base only the size counts.
+struct Carve {
+    char *base;
+    size_t at = 0;
+    template <class T = void>
+    T *take(size_t bytes) {
+        char *q = base ? base + at : nullptr;
+        at = align_up(at + bytes, 256);
+        return (T *)q;
+    }
+};
+
+bool fn_ok(int fn) { return fn >= MOE_FN_NONE && fn <= MOE_FN_RELU; }
+template <class... P>
+bool aligned16(P... p) {
+    return (((uintptr_t)p | ...) & 15) == 0;
+}
+bool fits31(int64_t a, int64_t b) { return a * b < INT32_MAX; }
+
+moe_status check_ws(const char *who, const void *ws, size_t have, size_t need) {
+    if (need == 0) return MOE_OK;
+    if (ws == nullptr || have < need) {
+        set_error("%s: workspace of %zu bytes needed, got %zu", who, need, ws ? have : (size_t)0);
+        return MOE_ERR_WORKSPACE;
+    }
+    MOE_REQUIRE(aligned16(ws), "%s: the workspace must be 16-byte aligned", who);
+    return MOE_OK;
+}
+
+// ------------------------------------------------------------------ linear
+
+moe_status check_linear(const char *who, const moe_linear_desc *d, bool backward) {
+    MOE_REQUIRE(d != nullptr, "%s: NULL descriptor", who);
+    MOE_REQUIRE(d->T >= 0 && d->n > 0 && d->kdim > 0 && d->kdim % 8 == 0,
+                "%s: need T >= 0, n > 0, kdim > 0 and a multiple of 8 (T=%d n=%d kdim=%d)", who, d->T, d->n, d->kdim);
+    MOE_REQUIRE(fn_ok(d->fn), "%s: unknown activation %d", who, d->fn);
+    if (backward) {
+        MOE_REQUIRE(d->x_dtype == MOE_DT_BF16 || d->x_dtype == MOE_DT_MXFP8, "%s: x_dtype %d is neither bf16 nor MXFP8", who,
+                    d->x_dtype);
+        MOE_REQUIRE(d->x_dtype != MOE_DT_MXFP8 || d->kdim % 32 == 0, "%s: MXFP8 kdim = %d is not a multiple of 32", who,
+                    d->kdim);
+    } else {
+        MOE_REQUIRE(d->x_dtype == MOE_DT_BF16 || d->x_dtype == MOE_DT_F32, "%s: unknown x_dtype %d", who, d->x_dtype);
+        MOE_REQUIRE(d->y_dtype == MOE_DT_BF16 || d->y_dtype == MOE_DT_F32, "%s: unknown y_dtype %d", who, d->y_dtype);
+    }
+    MOE_REQUIRE(fits31(d->T, d->n + 8) && fits31(d->n, d->kdim) && fits31(d->T, d->kdim), "%s: sizes overflow int32", who);
+    return MOE_OK;
+}
+
+struct LinearWs {
+    DensePlan plan;
+    uint16_t *planes;
+    float *part;
+    size_t bytes;
+};
+LinearWs linear_ws(const moe_linear_desc *d, void *base) {
+    LinearWs w = {};
+    if (d->T <= kGemvTokens) return w;
+    const bool f32 = d->x_dtype == MOE_DT_F32;
+    Carve c{(char *)base};
+    w.plan = dense_plan(kFormNT, false, d->T, d->n, d->kdim, f32 ? 3 : 1);
+    w.planes = c.take<uint16_t>(f32 ? (size_t)3 * d->T * d->kdim * 2 : 0);
+    w.part = c.take<float>(dense_plan_bytes(w.plan, false, d->T, d->n));
+    w.bytes = c.at;
+    return w;
+}
+
+struct LinearBwdWs {
+    DensePlan pz, px, pw;
+    uint16_t *x, *dz;
+    float *cs, *part;
+    int ldz, csld, cs_rows;
+    bool own_dz;
+    size_t bytes;
+};
+LinearBwdWs linear_bwd_ws(const moe_linear_desc *d, void *base) {
+    LinearBwdWs w = {};
+    Carve c{(char *)base};
+    const bool act = d->fn != MOE_FN_NONE;
+    w.ldz = (d->n + 7) & ~7;
+    w.csld = w.ldz;
+    w.own_dz = act || w.ldz != d->n;       // dy itself serves as dz otherwise
+    w.pz = dense_plan(kFormNT, false, d->T, d->n, d->kdim, 1);
+    w.px = dense_plan(kFormNN, false, d->T, d->kdim, d->n, 1);
+    w.pw = dense_plan(kFormTN, false, d->n, d->kdim, d->T, 1);
+    w.cs_rows = act ? w.pz.cs_rows : (d->T + kColRows - 1) / kColRows;
+    w.x = c.take<uint16_t>(d->x_dtype == MOE_DT_MXFP8 ? (size_t)d->T * d->kdim * 2 : 0);
+    w.dz = c.take<uint16_t>(w.own_dz ? (size_t)d->T * w.ldz * 2 : 0);
+    w.cs = c.take<float>((size_t)w.cs_rows * w.csld * 4);
+    size_t part = act ? dense_plan_bytes(w.pz, false, d->T, d->n) : 0;
+    const size_t bx = dense_plan_bytes(w.px, false, d->T, d->kdim), bw = dense_plan_bytes(w.pw, false, d->n, d->kdim);
+    part = part > bx ? part : bx;
+    part = part > bw ? part : bw;
+    w.part = c.take<float>(part);
+    w.bytes = c.at;
+    return w;
+}
+
+// ------------------------------------------------------------------ gated
+
+moe_status check_gateup(const char *who, const moe_gateup_desc *d, bool backward) {
+    MOE_REQUIRE(d != nullptr, "%s: NULL descriptor", who);
+    MOE_REQUIRE(d->T >= 0 && d->d_model > 0 && d->d_model % 8 == 0 && d->d_ff > 0 && d->d_ff % 8 == 0,
+                "%s: need T >= 0 and d_model, d_ff positive multiples of 8 (T=%d d_model=%d d_ff=%d)", who, d->T, d->d_model,
+                d->d_ff);
+    MOE_REQUIRE(fn_ok(d->fn), "%s: unknown activation %d", who, d->fn);
+    if (backward) {
+        MOE_REQUIRE(d->x_dtype == MOE_DT_BF16 || d->x_dtype == MOE_DT_MXFP8, "%s: x_dtype %d is neither bf16 nor MXFP8", who,
+                    d->x_dtype);
+        MOE_REQUIRE(d->x_dtype != MOE_DT_MXFP8 || d->d_model % 32 == 0, "%s: MXFP8 d_model = %d is not a multiple of 32", who,
+                    d->d_model);
+    } else {
+        MOE_REQUIRE(d->x_dtype == MOE_DT_BF16, "%s: x must be bf16 (x_dtype %d)", who, d->x_dtype);
+        MOE_REQUIRE(d->h_dtype == MOE_DT_BF16 || d->h_dtype == MOE_DT_F32, "%s: unknown h_dtype %d", who, d->h_dtype);
+    }
+    MOE_REQUIRE(d->d_ff < INT32_MAX / 2 && fits31(d->T, 2 * d->d_ff) && fits31(d->d_model, 2 * d->d_ff) &&
+                    fits31(d->T, d->d_model),
+                "%s: sizes overflow int32", who);
+    return MOE_OK;
+}
+
+struct GateWs {
+    DensePlan plan;
+    float *part;
+    size_t bytes;
+};
+GateWs gate_ws(const moe_gateup_desc *d, void *base) {
+    GateWs w = {};
+    if (d->T <= kGemvTokens) return w;
+    Carve c{(char *)base};
+    w.plan = dense_plan(kFormNT, true, d->T, d->d_ff, d->d_model, 1);
+    w.part = c.take<float>(dense_plan_bytes(w.plan, true, d->T, d->d_ff));
+    w.bytes = c.at;
+    return w;
+}
+
+struct GateBwdWs {
+    DensePlan pg, px, pw;
+    uint16_t *x, *dgu;
+    float *cs, *part;
+    int cs_rows;                 // with recomputed pre-activations
+    int cs_rows_saved;
+    size_t bytes;
+};
+GateBwdWs gate_bwd_ws(const moe_gateup_desc *d, void *base) {
+    GateBwdWs w = {};
+    Carve c{(char *)base};
+    const int f = d->d_ff;
+    w.pg = dense_plan(kFormNT, true, d->T, f, d->d_model, 1);
+    w.px = dense_plan(kFormNN, false, d->T, d->d_model, f, 2);
+    w.pw = dense_plan(kFormTN, false, 2 * f, d->d_model, d->T, 1);
+    w.cs_rows = w.pg.cs_rows;
+    w.cs_rows_saved = (d->T + kFinishRows - 1) / kFinishRows;
+    w.x = c.take<uint16_t>(d->x_dtype == MOE_DT_MXFP8 ? (size_t)d->T * d->d_model * 2 : 0);
+    w.dgu = c.take<uint16_t>((size_t)d->T * 2 * f * 2);
+    w.cs = c.take<float>((size_t)(w.cs_rows > w.cs_rows_saved ? w.cs_rows : w.cs_rows_saved) * 2 * f * 4);
+    size_t part = dense_plan_bytes(w.pg, true, d->T, f);
+    const size_t bx = dense_plan_bytes(w.px, false, d->T, d->d_model), bw = dense_plan_bytes(w.pw, false, 2 * f, d->d_model);
+    part = part > bx ? part : bx;
+    part = part > bw ? part : bw;
+    w.part = c.take<float>(part);
+    w.bytes = c.at;
+    return w;
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" size_t moe_dense_linear_workspace(const moe_linear_desc *d) {
+    return check_linear("moe_dense_linear_workspace", d, false) == MOE_OK ? linear_ws(d, nullptr).bytes : 0;
+}
+
+extern "C" moe_status moe_dense_linear(const moe_linear_desc *d, const void *x, const void *w, const float *bias,
+                                       const void *residual, void *y, void *ws, size_t ws_bytes, moe_stream stream) {
+    clear_error();
+    MOE_TRY(check_linear("moe_dense_linear", d, false));
+    if (d->T == 0) return MOE_OK;
+    MOE_REQUIRE(x && w && y, "moe_dense_linear: NULL x, w or y");
+    MOE_REQUIRE(aligned16(x, w, bias, residual, y), "moe_dense_linear: tensors must be 16-byte aligned");
+    const LinearWs b = linear_ws(d, ws);
+    MOE_TRY(check_ws("moe_dense_linear", ws, ws_bytes, b.bytes));
+    hipStream_t s = (hipStream_t)stream;
+    const bool f32 = d->x_dtype == MOE_DT_F32;
+    EpiLinear e;
+    e.bias = bias;
+    e.res = residual;
+    e.y = y;
+    e.C = d->n;
+    e.fn = d->fn;
+    e.y_f32 = d->y_dtype == MOE_DT_F32;
+    if (d->T <= kGemvTokens) return dense_linear_gemv(x, f32, (const uint16_t *)w, d->T, d->n, d->kdim, e, s);
+    const size_t plane = (size_t)d->T * d->kdim;
+    if (f32) MOE_TRY(dense_split3((const float *)x, b.planes, plane, s));
+    DenseProduct p = {};
+    p.nseg = f32 ? 3 : 1;
+    for (int i = 0; i < p.nseg; ++i) {
+        p.rp[i] = f32 ? b.planes + i * plane : (const uint16_t *)x;
+        p.cp[i] = (const uint16_t *)w;
+    }
+    p.K = p.ldr = p.ldc = d->kdim;
+    p.R = d->T;
+    p.C = d->n;
+    return dense_linear_product(p, b.plan, e, b.part, s);
+}
+
+extern "C" size_t moe_dense_linear_backward_workspace(const moe_linear_desc *d) {
+    return check_linear("moe_dense_linear_backward_workspace", d, true) == MOE_OK ? linear_bwd_ws(d, nullptr).bytes : 0;
+}
+
+extern "C" moe_status moe_dense_linear_backward(const moe_linear_desc *d, const void *dy, const void *x,
+                                                const uint8_t *x_scales, const void *w, const float *bias, void *dx,
+                                                void *dw, float *dbias, void *ws, size_t ws_bytes, moe_stream stream) {
+    clear_error();
+    MOE_TRY(check_linear("moe_dense_linear_backward", d, true));
+    MOE_REQUIRE(dx || dw || dbias, "moe_dense_linear_backward: no gradient asked for");
+    const bool act = d->fn != MOE_FN_NONE, mx = d->x_dtype == MOE_DT_MXFP8;
+    const bool need_x = act || dw, need_w = act || dx;
+    if (d->T > 0) {
+        MOE_REQUIRE(dy && (x || !need_x) && (w || !need_w), "moe_dense_linear_backward: NULL dy, x or w");
+        MOE_REQUIRE(!(mx && need_x && !x_scales), "moe_dense_linear_backward: MXFP8 x without x_scales");
+    }
+    MOE_REQUIRE(aligned16(dy, x, w, bias, dx, dw, dbias), "moe_dense_linear_backward: tensors must be 16-byte aligned");
+    const LinearBwdWs b = linear_bwd_ws(d, ws);
+    MOE_TRY(check_ws("moe_dense_linear_backward", ws, ws_bytes, b.bytes));
+    hipStream_t s = (hipStream_t)stream;
+    const int T = d->T, n = d->n, k = d->kdim;
+    const uint16_t *xb = (const uint16_t *)x;
+    if (T > 0 && mx && need_x) {
+        MOE_TRY(mxfp8_dequant_launch((size_t)T, k, (const uint8_t *)x, x_scales, b.x, false, s));
+        xb = b.x;
+    }
+    const uint16_t *dz = (const uint16_t *)dy;
+    if (T > 0 && act) {
+        DenseProduct p = {};
+        p.nseg = 1;
+        p.rp[0] = xb;
+        p.cp[0] = (const uint16_t *)w;
+        p.K = p.ldr = p.ldc = k;
+        p.R = T;
+        p.C = n;
+        EpiLinearBwd e;
+        e.bias = bias;
+        e.dy = dz;
+        e.dz = b.dz;
+        e.C = n;
+        e.ldz = b.ldz;
+        e.fn = d->fn;
+        e.cs = dbias ? b.cs : nullptr;
+        e.csld = b.csld;
+        MOE_TRY(dense_linear_bwd_product(p, b.pz, e, b.part, s));
+        dz = b.dz;
+    } else if (T > 0) {
+        if (dbias) MOE_TRY(dense_colsum(dz, T, n, b.cs, b.csld, s));
+        if (b.own_dz && (dx || dw)) {
+            MOE_TRY(dense_pad_rows(dz, b.dz, T, n, b.ldz, s));
+            dz = b.dz;
+        }
+    }
+    if (dbias) MOE_TRY(dense_colsum_reduce(b.cs, T > 0 ? b.cs_rows : 0, b.csld, n, dbias, nullptr, s));
+    if (dx && T > 0) {
+        DenseProduct p = {};
+        p.nseg = 1;
+        p.rp[0] = dz;
+        p.cp[0] = (const uint16_t *)w;
+        p.K = n;
+        p.ldr = b.ldz;
+        p.ldc = k;
+        p.R = T;
+        p.C = k;
+        EpiStore e;
+        e.out0 = (uint16_t *)dx;
+        e.out1 = nullptr;
+        e.rows0 = T;
+        e.C = k;
+        MOE_TRY(dense_nn_product(p, b.px, e, b.part, s));
+    }
+    if (dw) {
+        DenseProduct p = {};
+        p.nseg = 1;
+        p.rp[0] = dz;
+        p.cp[0] = xb;
+        p.K = T;
+        p.ldr = b.ldz;
+        p.ldc = k;
+        p.R = n;
+        p.C = k;
+        p.rcols = b.ldz;
+        EpiStore e;
+        e.out0 = (uint16_t *)dw;
+        e.out1 = nullptr;
+        e.rows0 = n;
+        e.C = k;
+        MOE_TRY(dense_tn_product(p, b.pw, e, b.part, s));
+    }
+    return MOE_OK;
+}
+
+extern "C" size_t moe_dense_gateup_workspace(const moe_gateup_desc *d) {
+    return check_gateup("moe_dense_gateup_workspace", d, false) == MOE_OK ? gate_ws(d, nullptr).bytes : 0;
+}
+
+extern "C" moe_status moe_dense_gateup(const moe_gateup_desc *d, const void *x, const void *w_gate, const void *w_up,
+                                       const float *b_gate, const float *b_up, void *h, void *pre, void *ws,
+                                       size_t ws_bytes, moe_stream stream) {
+    clear_error();
+    MOE_TRY(check_gateup("moe_dense_gateup", d, false));
+    if (d->T == 0) return MOE_OK;
+    MOE_REQUIRE(x && w_gate && w_up && h, "moe_dense_gateup: NULL x, w_gate, w_up or h");
+    MOE_REQUIRE(aligned16(x, w_gate, w_up, b_gate, b_up, h, pre), "moe_dense_gateup: tensors must be 16-byte aligned");
+    const GateWs b = gate_ws(d, ws);
+    MOE_TRY(check_ws("moe_dense_gateup", ws, ws_bytes, b.bytes));
+    EpiGate e;
+    e.bg = b_gate;
+    e.bu = b_up;
+    e.h = h;
+    e.pre = (uint16_t *)pre;
+    e.plane = (size_t)d->T * d->d_ff;
+    e.C = d->d_ff;
+    e.fn = d->fn;
+    e.h_f32 = d->h_dtype == MOE_DT_F32;
+    hipStream_t s = (hipStream_t)stream;
+    const uint16_t *xb = (const uint16_t *)x, *wg = (const uint16_t *)w_gate, *wu = (const uint16_t *)w_up;
+    if (d->T <= kGemvTokens) return dense_gate_gemv(xb, wg, wu, d->T, d->d_ff, d->d_model, e, s);
+    DenseProduct p = {};
+    p.nseg = 1;
+    p.rp[0] = xb;
+    p.cp[0] = wg;
+    p.cp[1] = wu;
+    p.K = p.ldr = p.ldc = d->d_model;
+    p.R = d->T;
+    p.C = d->d_ff;
+    return dense_gate_product(p, b.plan, e, b.part, s);
+}
+
+extern "C" size_t moe_dense_gateup_backward_workspace(const moe_gateup_desc *d) {
+    return check_gateup("moe_dense_gateup_backward_workspace", d, true) == MOE_OK ? gate_bwd_ws(d, nullptr).bytes : 0;
+}
+
+extern "C" moe_status moe_dense_gateup_backward(const moe_gateup_desc *d, const void *dh, const void *x,
+                                                const uint8_t *x_scales, const void *w_gate, const void *w_up,
+                                                const float *b_gate, const float *b_up, const void *pre, void *dx,
+                                                void *dw_gate, void *dw_up, float *db_gate, float *db_up, void *h,
+                                                void *ws, size_t ws_bytes, moe_stream stream) {
+    clear_error();
+    MOE_TRY(check_gateup("moe_dense_gateup_backward", d, true));
+    MOE_REQUIRE(!dw_gate == !dw_up && !db_gate == !db_up,
+                "moe_dense_gateup_backward: the gate's and up's gradients come together");
+    MOE_REQUIRE(dx || dw_gate || db_gate || h, "moe_dense_gateup_backward: no result asked for");
+    const bool mx = d->x_dtype == MOE_DT_MXFP8, need_x = !pre || dw_gate;
+    if (d->T > 0) {
+        MOE_REQUIRE(dh && w_gate && w_up && (x || !need_x), "moe_dense_gateup_backward: NULL dh, x, w_gate or w_up");
+        MOE_REQUIRE(!(mx && need_x && !x_scales), "moe_dense_gateup_backward: MXFP8 x without x_scales");
+    }
+    MOE_REQUIRE(aligned16(dh, x, w_gate, w_up, b_gate, b_up, pre, dx, dw_gate, dw_up, db_gate, db_up, h),
+                "moe_dense_gateup_backward: tensors must be 16-byte aligned");
+    const GateBwdWs b = gate_bwd_ws(d, ws);
+    MOE_TRY(check_ws("moe_dense_gateup_backward", ws, ws_bytes, b.bytes));
+    hipStream_t s = (hipStream_t)stream;
+    const int T = d->T, f = d->d_ff, dm = d->d_model;
+    const uint16_t *xb = (const uint16_t *)x, *wg = (const uint16_t *)w_gate, *wu = (const uint16_t *)w_up;
+    if (T > 0 && mx && need_x) {
+        MOE_TRY(mxfp8_dequant_launch((size_t)T, dm, (const uint8_t *)x, x_scales, b.x, false, s));
+        xb = b.x;
+    }
+    if (T > 0) {
+        EpiGateBwd e;
+        e.bg = b_gate;
+        e.bu = b_up;
+        e.dh = (const uint16_t *)dh;
+        e.dgu = b.dgu;
+        e.h = (uint16_t *)h;
+        e.C = f;
+        e.fn = d->fn;
+        e.cs = db_gate ? b.cs : nullptr;
+        e.csld = 2 * f;
+        if (pre) {
+            MOE_TRY(dense_gate_bwd_saved(e, (const uint16_t *)pre, T, s));
+        } else {
+            DenseProduct p = {};
+            p.nseg = 1;
+            p.rp[0] = xb;
+            p.cp[0] = wg;
+            p.cp[1] = wu;
+            p.K = p.ldr = p.ldc = dm;
+            p.R = T;
+            p.C = f;
+            MOE_TRY(dense_gate_bwd_product(p, b.pg, e, b.part, s));
+        }
+    }
+    if (db_gate)
+        MOE_TRY(dense_colsum_reduce(b.cs, T == 0 ? 0 : (pre ? b.cs_rows_saved : b.cs_rows), 2 * f, f, db_gate, db_up, s));
+    if (dx && T > 0) {
+        DenseProduct p = {};
+        p.nseg = 2;
+        p.rp[0] = b.dgu;
+        p.rp[1] = b.dgu + f;
+        p.cp[0] = wg;
+        p.cp[1] = wu;
+        p.K = f;
+        p.ldr = 2 * f;
+        p.ldc = dm;
+        p.R = T;
+        p.C = dm;
+        EpiStore e;
+        e.out0 = (uint16_t *)dx;
+        e.out1 = nullptr;
+        e.rows0 = T;
+        e.C = dm;
+        MOE_TRY(dense_nn_product(p, b.px, e, b.part, s));
+    }
+    if (dw_gate) {
+        DenseProduct p = {};
+        p.nseg = 1;
+        p.rp[0] = b.dgu;
+        p.cp[0] = xb;
+        p.K = T;
+        p.ldr = 2 * f;
+        p.ldc = dm;
+        p.R = 2 * f;
+        p.C = dm;
+        p.rcols = 2 * f;
+        EpiStore e;
+        e.out0 = (uint16_t *)dw_gate;
+        e.out1 = (uint16_t *)dw_up;
+        e.rows0 = f;
+        e.C = dm;
+        MOE_TRY(dense_tn_product(p, b.pw, e, b.part, s));
+    }
+    return MOE_OK;
+}

@@ -1,0 +1,330 @@
+// The dense bf16 product kernel on the matrix cores (see dense.h for the products).
+//
+// A workgroup computes one BR x BC tile of the output; each wave owns a (16 TR) x (16 TC) part as
+// MFMA tiles.  The columns operand is the MFMA's first operand and the rows operand its second,
+// so a lane's four accumulators are four consecutive columns of one row.  The sum advances in
+// steps of 64 values, both operands of a step in LDS, two steps resident: step s+1 is copied
+// global -> LDS (no registers) while step s is multiplied; one barrier a step.
+//
+// LDS of a step.  An operand contiguous along the sum is kept as rows of 64 values (128 bytes),
+// 16-byte chunk c of row r at position c ^ ((r >> 1) & 7): an operand read takes one chunk of 16
+// rows and touches each 16-byte bank group once.  An operand strided along the sum is kept as it
+// lies in memory, 64 rows (one per value of the sum) of BR or BC values, and read with the
+// transposing LDS read (ds_read_b64_tr_b16): a group of 16 lanes supplies 4 rows of 16 values and
+// lane i receives column i of the four.  Its 16-byte chunk c of row k sits at c ^ 2g(k), g(k) =
+// (k & 3) | ((k >> 3) & 1) << 2: the eight 32-byte row pieces that half a wave reads then fall on
+// eight different bank groups.
+//
+// Values past the end of the sum are copied from a zero page (for both operands), rows past the
+// end of a matrix repeat its last row and their results are not stored.
+#pragma once
+#include "dense.h"
+
+namespace moe {
+
+struct CfgL { static constexpr int BR = 256, BC = 256, WR = 2, WC = 4; };   // 8 waves of 128 x 64
+struct CfgM { static constexpr int BR = 128, BC = 128, WR = 2, WC = 2; };   // 4 waves of 64 x 64
+struct CfgS { static constexpr int BR = 64, BC = 128, WR = 1, WC = 4; };    // 4 waves of 64 x 32
+
+constexpr int kBK = 64;
+
+struct GemmArgs {
+    DenseProduct p;
+    int tr, tc, split, steps, seg_steps;
+};
+
+__device__ __attribute__((aligned(16))) const uint32_t g_dense_zero[4] = {0, 0, 0, 0};
+
+// global -> LDS copies, 16 bytes a lane, to dst + 16 lane (asm: the compiler would otherwise wait for
+// all copies in flight before every LDS read; the loop waits for exactly what it needs).
+MOE_DEV void copy16(const void *base, uint32_t voff, uint32_t lds) {
+    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds) : "memory");
+}
+MOE_DEV void copy16_addr(const void *src, uint32_t lds) {
+    asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(lds) : "memory");
+}
+MOE_DEV const uint16_t *uniform16(const uint16_t *q) {
+    const uint64_t v = (uint64_t)(uintptr_t)q;
+    const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+    return (const uint16_t *)(uintptr_t)(((uint64_t)hi << 32) | lo);
+}
+
+MOE_DEV int ks_swz(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) << 1; }
+
+// One operand's tile of N free indices: copies of a step and MFMA operand reads.
+template <bool STRIDED, int N, int NW>
+struct Operand {
+    static constexpr int kBytes = N * kBK * 2;                // of one step
+    static constexpr int kCopies = kBytes / 1024 / NW;        // copy instructions per wave and step
+    static_assert(kBytes % (1024 * NW) == 0, "whole copies per wave");
+    static_assert(!STRIDED || N >= 128, "the chunk permutation of strided rows spans 16 chunks");
+    uint32_t voff[kCopies];
+
+    // this wave's copy t covers LDS bytes [(wave * kCopies + t) * 1024, +1024) of the step
+    static MOE_DEV int slot(int wave, int t) { return wave * kCopies + t; }
+    // contiguous: LDS row and chunk position of this lane's 16 bytes
+    static MOE_DEV int kc_row(int wave, int t, int lane) { return slot(wave, t) * 8 + (lane >> 3); }
+    static MOE_DEV int kc_chunk(int row, int lane) { return (lane & 7) ^ ((row >> 1) & 7); }
+    // strided: k within the step and chunk of this lane's 16 bytes
+    static constexpr int kRowLanes = N / 8;                   // lanes per k row
+    static MOE_DEV int ks_k(int wave, int t, int lane) { return slot(wave, t) * (64 / kRowLanes) + lane / kRowLanes; }
+    static MOE_DEV int ks_chunk(int k, int lane) { return (lane & (kRowLanes - 1)) ^ ks_swz(k); }
+};
+
+template <class Cfg, int FORM, class Epi>
+__global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const GemmArgs ga, Epi epi) {
+    constexpr int BR = Cfg::BR, BC = Cfg::BC, NW = Cfg::WR * Cfg::WC;
+    constexpr int TR = BR / Cfg::WR / 16, TC = BC / Cfg::WC / 16;
+    constexpr bool RS = FORM == kFormTN, CS = FORM != kFormNT, PAIR = Epi::kPair;
+    static_assert(!PAIR || FORM == kFormNT, "pairs are forward products");
+    using OpR = Operand<RS, BR, NW>;
+    using OpC = Operand<CS, BC, NW>;
+    constexpr int kStage = OpR::kBytes + OpC::kBytes;
+    extern __shared__ __align__(16) unsigned char smem[];
+
+    const DenseProduct &p = ga.p;
+    const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
+    const int wr = wave / Cfg::WC, wc = wave % Cfg::WC;
+    const int lr = lane & 15, lg = lane >> 4;
+
+    // ---- which tile: XCD x (workgroups x, x + 8, ...) takes a contiguous run of the order below,
+    // in which kGroup row tiles share each column tile, so the tiles that run together on an XCD
+    // form a block and share both operands in its L2.
+    constexpr int kGroup = 4;
+    const int tiles = ga.tr * ga.tc, G = tiles * ga.split;
+    int slot;
+    {
+        const int b = blockIdx.x, x = b & 7, q = G >> 3, rem = G & 7;
+        slot = x * q + min(x, rem) + (b >> 3);
+    }
+    const int sp = slot / tiles;
+    int tr, tc;
+    {
+        const int t = slot - sp * tiles, per = kGroup * ga.tc, g = t / per, i = t - g * per;
+        const int gr = min(kGroup, ga.tr - g * kGroup);
+        tr = g * kGroup + i % gr;
+        tc = i / gr;
+    }
+    constexpr int kPairCols = BC / 2;                       // columns of each matrix in a pair tile
+    const int r0 = tr * BR, c0 = tc * (PAIR ? kPairCols : BC);
+    const int s0 = (int)((int64_t)ga.steps * sp / ga.split), s1 = (int)((int64_t)ga.steps * (sp + 1) / ga.split);
+
+    // ---- copy sources
+    OpR opr;
+    OpC opc;
+#pragma unroll
+    for (int t = 0; t < OpR::kCopies; ++t) {
+        if constexpr (!RS) {
+            const int row = OpR::kc_row(wave, t, lane);
+            opr.voff[t] = 2u * ((uint32_t)min(row, p.R - 1 - r0) * (uint32_t)p.ldr + 8u * OpR::kc_chunk(row, lane));
+        } else {
+            const int k = OpR::ks_k(wave, t, lane);
+            opr.voff[t] = 2u * ((uint32_t)k * (uint32_t)p.ldr + (uint32_t)min(8 * OpR::ks_chunk(k, lane), p.rcols - 8 - r0));
+        }
+    }
+    // pair tile: LDS row j of the columns operand is, within wave wc's 16 TC rows, gate column
+    // j % (8 TC) in the first half and up column in the second
+    constexpr int kWCols = 16 * TC, kHalf = 8 * TC;
+    auto pair_mat = [&](int row) { return (row % kWCols) / kHalf; };
+    auto pair_col = [&](int row) { return row / kWCols * kHalf + row % kHalf; };
+#pragma unroll
+    for (int t = 0; t < OpC::kCopies; ++t) {
+        if constexpr (!CS) {
+            const int row = OpC::kc_row(wave, t, lane);
+            const int col = PAIR ? pair_col(row) : row;
+            opc.voff[t] = 2u * ((uint32_t)min(col, p.C - 1 - c0) * (uint32_t)p.ldc + 8u * OpC::kc_chunk(row, lane));
+        } else {
+            const int k = OpC::ks_k(wave, t, lane);
+            opc.voff[t] = 2u * ((uint32_t)k * (uint32_t)p.ldc + (uint32_t)min(8 * OpC::ks_chunk(k, lane), p.C - 8 - c0));
+        }
+    }
+
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
+    // copies of step s into stage st
+    auto issue = [&](int s, int st) {
+        const int seg = s / ga.seg_steps, k0 = (s - seg * ga.seg_steps) * kBK;
+        const uint16_t *rb = seg == 0 ? p.rp[0] : (seg == 1 ? p.rp[1] : p.rp[2]);
+        const uint16_t *cb = PAIR ? p.cp[0] : (seg == 0 ? p.cp[0] : (seg == 1 ? p.cp[1] : p.cp[2]));
+        rb += RS ? (size_t)k0 * p.ldr + r0 : (size_t)r0 * p.ldr + k0;
+        cb += CS ? (size_t)k0 * p.ldc + c0 : (size_t)c0 * p.ldc + k0;
+        const uint16_t *ub = PAIR ? p.cp[1] + ((size_t)c0 * p.ldc + k0) : nullptr;
+        const uint32_t lr_ = lds0 + st * kStage + OpR::slot(wave, 0) * 1024;
+        const uint32_t lc_ = lds0 + st * kStage + OpR::kBytes + OpC::slot(wave, 0) * 1024;
+        const int live = p.K - k0;                           // values of the sum left in this segment
+        if (live >= kBK) {
+            const uint16_t *rbu = uniform16(rb);
+#pragma unroll
+            for (int t = 0; t < OpR::kCopies; ++t) copy16(rbu, opr.voff[t], lr_ + t * 1024);
+#pragma unroll
+            for (int t = 0; t < OpC::kCopies; ++t) {
+                const uint16_t *b = cb;
+                if constexpr (PAIR) b = pair_mat(OpC::slot(wave, t) * 8) ? ub : cb;
+                copy16(uniform16(b), opc.voff[t], lc_ + t * 1024);
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < OpR::kCopies; ++t) {
+                const int row = OpR::kc_row(wave, t, lane);
+                const int k = RS ? OpR::ks_k(wave, t, lane) : 8 * OpR::kc_chunk(row, lane);
+                const void *a = (const char *)rb + opr.voff[t];
+                copy16_addr(k < live ? a : (const void *)g_dense_zero, lr_ + t * 1024);
+            }
+#pragma unroll
+            for (int t = 0; t < OpC::kCopies; ++t) {
+                const int row = OpC::kc_row(wave, t, lane);
+                const int k = CS ? OpC::ks_k(wave, t, lane) : 8 * OpC::kc_chunk(row, lane);
+                const uint16_t *b = cb;
+                if constexpr (PAIR) b = pair_mat(OpC::slot(wave, t) * 8) ? ub : cb;
+                const void *a = (const char *)b + opc.voff[t];
+                copy16_addr(k < live ? a : (const void *)g_dense_zero, lc_ + t * 1024);
+            }
+        }
+    };
+
+    f32x4 acc[TC][TR];
+#pragma unroll
+    for (int i = 0; i < TC; ++i)
+#pragma unroll
+        for (int j = 0; j < TR; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    typedef short s16x4 __attribute__((ext_vector_type(4)));
+    typedef short s16x8 __attribute__((ext_vector_type(8)));
+    // MFMA operand of free indices f0 .. f0+15 (f0 a multiple of 16), values 32 ks + 8 lg .. +7
+    auto frag_c = [&](int base, int f0, int ks) {            // contiguous
+        const int at = base + f0 * 128 + lr * 128 + (((4 * ks + lg) ^ (lr >> 1)) << 4);
+        return *(const bf16x8 *)(smem + at);
+    };
+    auto frag_s = [&](int base, int f0, int ks, auto width) { // strided
+        constexpr int W = decltype(width)::value;            // free indices of the tile
+        const int k = 32 * ks + 8 * lg + (lr >> 2);
+        const int chunk = ((f0 >> 3) + ((lr & 3) >> 1)) ^ ks_swz(k);
+        const int at = base + k * (2 * W) + chunk * 16 + (lr & 1) * 8;
+        typedef __attribute__((address_space(3))) s16x4 lds4;
+        const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(uintptr_t)(lds0 + at));
+        const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(uintptr_t)(lds0 + at + 4 * 2 * W));
+        const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        return __builtin_bit_cast(bf16x8, v);
+    };
+    auto compute = [&](int st) {
+        const int base_r = st * kStage, base_c = st * kStage + OpR::kBytes;
+#pragma unroll
+        for (int ks = 0; ks < kBK / 32; ++ks) {
+            bf16x8 fr[TR], fc[TC];
+#pragma unroll
+            for (int j = 0; j < TR; ++j) {
+                const int f0 = wr * 16 * TR + 16 * j;
+                if constexpr (RS) fr[j] = frag_s(base_r, f0, ks, std::integral_constant<int, BR>{});
+                else fr[j] = frag_c(base_r, f0, ks);
+            }
+#pragma unroll
+            for (int i = 0; i < TC; ++i) {
+                const int f0 = wc * 16 * TC + 16 * i;
+                if constexpr (CS) fc[i] = frag_s(base_c, f0, ks, std::integral_constant<int, BC>{});
+                else fc[i] = frag_c(base_c, f0, ks);
+            }
+#pragma unroll
+            for (int i = 0; i < TC; ++i)
+#pragma unroll
+                for (int j = 0; j < TR; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc[i], fr[j], acc[i][j], 0, 0, 0);
+        }
+    };
+
+    if (s0 < s1) issue(s0, 0);
+    for (int s = s0; s < s1; ++s) {
+        // this wave's copies of step s have landed and its reads of step s-1 are done; then all meet
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (s + 1 < s1) issue(s + 1, (s + 1 - s0) & 1);
+        compute((s - s0) & 1);
+    }
+
+    // ---- epilogue.  Lane (lr, lg) of MFMA tile (i, j) holds columns 4 lg .. 4 lg + 3 of row lr.  The
+    // wave's tile goes through LDS (64 rows at a time, 16-byte chunk c of row r at c ^ (r & 15 or 7)) so
+    // that 8 or 16 neighbouring lanes take one row: whole lines are read and written, and the
+    // epilogue's code appears once.
+    if constexpr (std::is_same_v<Epi, EpiPartial<PAIR>>) epi.part += (size_t)sp * epi.plane * (PAIR ? 2 : 1);
+    constexpr int kCh = 4 * TC;                              // 16-byte chunks of a float32 row of the wave's tile
+    constexpr int kJP = TR < 4 ? TR : 4;                     // MFMA tile rows per pass
+    constexpr int kLanes = PAIR ? kCh / 2 : kCh, kRows = 64 / kLanes;
+    static_assert(NW * kJP * 16 * kCh * 16 <= 2 * kStage, "the passes fit in the operands' LDS");
+    static_assert(kCh == 8 || kCh == 16, "chunk permutation");
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");    // every wave has read its last operands
+    unsigned char *mine = smem + wave * (kJP * 16 * kCh * 16);
+    const int ec = lane % kLanes, er = lane / kLanes;
+    const int c = c0 + wc * (PAIR ? kHalf : kWCols) + 4 * ec;
+    f32x4 sa = {0.f, 0.f, 0.f, 0.f}, sb = {0.f, 0.f, 0.f, 0.f};
+    static_for<TR / kJP>([&](auto pass) {
+#pragma unroll
+        for (int j = 0; j < kJP; ++j)
+#pragma unroll
+            for (int i = 0; i < TC; ++i)
+                *(f32x4 *)(mine + (16 * j + lr) * (kCh * 16) + (((4 * i + lg) ^ (lr & (kCh - 1))) << 4)) =
+                    acc[i][pass * kJP + j];
+#pragma unroll 2
+        for (int it = 0; it < kJP * 16 / kRows; ++it) {
+            const int row = it * kRows + er;
+            const int r = r0 + wr * 16 * TR + pass * kJP * 16 + row;
+            if (r < p.R && c < p.C) {
+                const unsigned char *src = mine + row * (kCh * 16);
+                const f32x4 a = *(const f32x4 *)(src + ((ec ^ (row & (kCh - 1))) << 4));
+                f32x4 b = a;
+                if constexpr (PAIR) b = *(const f32x4 *)(src + (((ec + kLanes) ^ (row & (kCh - 1))) << 4));
+                f32x4 ca = {0.f, 0.f, 0.f, 0.f}, cb = {0.f, 0.f, 0.f, 0.f};
+                epi.apply(r, c, a, b, ca, cb);
+                if constexpr (Epi::kColSum) {
+                    sa += ca;
+                    sb += cb;
+                }
+            }
+        }
+    });
+    if constexpr (Epi::kColSum) {
+        if (epi.cs) {
+            // the wave's 16 TR rows: one partial row per wave row of the grid
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int o = kLanes; o < 64; o <<= 1) {
+                    sa[q] += __shfl_xor(sa[q], o, kWave);
+                    if constexpr (PAIR) sb[q] += __shfl_xor(sb[q], o, kWave);
+                }
+            if (er == 0 && c < p.C) {
+                float *row = epi.cs + (size_t)(tr * Cfg::WR + wr) * epi.csld;
+                *(f32x4 *)(row + c) = sa;
+                if constexpr (PAIR) *(f32x4 *)(row + p.C + c) = sb;
+            }
+        }
+    }
+}
+
+template <class Cfg, int FORM, class Epi>
+moe_status dense_launch_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &e, hipStream_t s) {
+    constexpr int lds = 2 * (Cfg::BR + Cfg::BC) * kBK * 2;
+    GemmArgs ga{p, pl.tr, pl.tc, pl.split, pl.steps, (p.K + kBK - 1) / kBK};
+    auto kern = dense_gemm_kernel<Cfg, FORM, Epi>;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(pl.tr * pl.tc * pl.split)), dim3(64 * Cfg::WR * Cfg::WC), lds, s, ga, e);
+    return launch_check("dense product");
+}
+
+template <int FORM, class Epi>
+moe_status dense_launch(const DenseProduct &p, const DensePlan &pl, const Epi &e, hipStream_t s) {
+    if (pl.cfg == 0) return dense_launch_cfg<CfgL, FORM, Epi>(p, pl, e, s);
+    if constexpr (FORM != kFormTN)
+        if (pl.cfg == 2) return dense_launch_cfg<CfgS, FORM, Epi>(p, pl, e, s);
+    return dense_launch_cfg<CfgM, FORM, Epi>(p, pl, e, s);
+}
+
+// The product with its epilogue: in one kernel, or as parts summed by a second one.
+template <int FORM, class Epi>
+moe_status dense_run(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s) {
+    if (pl.split == 1) return dense_launch<FORM>(p, pl, e, s);
+    const int ld = (p.C + 3) & ~3;
+    EpiPartial<Epi::kPair> ep;
+    ep.part = part;
+    ep.plane = (size_t)p.R * ld;
+    ep.ld = ld;
+    MOE_TRY((dense_launch<FORM>(p, pl, ep, s)));
+    return dense_finish(pl, e, part, p.R, p.C, s);
+}
+
+}  // namespace moe

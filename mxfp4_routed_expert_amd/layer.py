@@ -217,3 +217,54 @@ class MoELayer:
         else:
             B.moe_combine(self.y_rows, self.p2r, self.topk_w, self.y_s, self.sg, out=self.out)
         return self.out
+
+
+class DenseFFN:
+    """A dense gated feed-forward block (bf16 weights): y = (act_fn(x Wg^T) * (x Wu^T)) Wd^T + residual, and its
+    training step.
+
+    forward(x, residual, train=True) keeps what backward(dy) needs: the input as it is (checkpoint="bf16": a reference,
+    so it must not change until backward has run) or in 8 bits (checkpoint="mxfp8": a copy of 33/64 of its bytes, which
+    stands for x in every gradient).  The backward pass recomputes the gate and up products from it.  Buffers for T
+    tokens are allocated once; results of a call are overwritten by the next."""
+
+    def __init__(self, w_gate, w_up, w_down, T: int, act_fn: str = "silu", checkpoint: str = "bf16"):
+        if checkpoint not in ("bf16", "mxfp8"):
+            raise ValueError(f"checkpoint must be 'bf16' or 'mxfp8' (got {checkpoint!r})")
+        f, d = w_gate.shape
+        if tuple(w_up.shape) != (f, d) or tuple(w_down.shape) != (d, f):
+            raise ValueError("w_gate and w_up are [d_ff][d_model], w_down is [d_model][d_ff]")
+        self.wg, self.wu, self.wd, self.T, self.act_fn = w_gate, w_up, w_down, T, act_fn
+        dev, mx = w_gate.device, checkpoint == "mxfp8"
+        if mx and d % 32 != 0:
+            raise ValueError(f"an MXFP8 checkpoint needs d_model a multiple of 32 (got {d})")
+        bf, u8 = torch.bfloat16, torch.uint8
+        e = lambda *s, dt=bf: torch.empty(s, dtype=dt, device=dev)
+        self.h, self.y = e(T, f), e(T, d)
+        self.x_saved = (e(T, d, dt=u8), e(T, d // 32, dt=u8)) if mx else None
+        self.saved = None                      # (x or codes, scales or None) of the last training forward
+        self.dh, self.dx = e(T, f), e(T, d)
+        self.dwg, self.dwu, self.dwd = e(f, d), e(f, d), e(d, f)
+        need = max(B.moe_dense_gateup_workspace(T, d, f, act_fn), B.moe_dense_linear_workspace(T, d, f),
+                   B.moe_dense_linear_backward_workspace(T, d, f),
+                   B.moe_dense_gateup_backward_workspace(T, d, f, act_fn, mx))
+        self.ws = B._workspace(need, dev)
+
+    def forward(self, x, residual=None, train: bool = False):
+        B.moe_dense_gateup(x, self.wg, self.wu, act_fn=self.act_fn, out=self.h, ws=self.ws)
+        B.moe_dense_linear(self.h, self.wd, residual=residual, out=self.y, ws=self.ws)
+        if train:
+            self.saved = B.moe_mxfp8_quantize(x, out=self.x_saved) if self.x_saved is not None else (x, None)
+        return self.y
+
+    def backward(self, dy):
+        """(dx, dw_gate, dw_up, dw_down) at dy; the residual's gradient is dy itself."""
+        if self.saved is None:
+            raise B.MoeError(B.MOE_ERR_INVALID_ARG, "DenseFFN.backward: no forward(..., train=True) before it")
+        x, xs = self.saved
+        B.moe_dense_linear_backward(dy, None, self.wd, want=("dx",), out=(self.dh, None, None), ws=self.ws)
+        B.moe_dense_gateup_backward(self.dh, x, self.wg, self.wu, act_fn=self.act_fn, x_scales=xs, want=("dx", "dw"),
+                                    want_h=True, out=(self.dx, self.dwg, self.dwu, None, None, self.h), ws=self.ws)
+        B.moe_dense_linear_backward(dy, self.h, self.wd, want=("dw",), out=(None, self.dwd, None), ws=self.ws)
+        self.saved = None
+        return self.dx, self.dwg, self.dwu, self.dwd
