@@ -395,20 +395,23 @@ moe_status moe_mx_quantize(int32_t rows, int32_t cols, const void *x, int32_t x_
  *   Ranges: up to 8 tokens read the weights once on the vector ALU and need no workspace; more run
  *   on the matrix cores, few tiles with the sum split over workgroups.
  * moe_dense_linear_backward -- with z = x W^T + bias and dz = dy f'(z):
- *   dx = dz W [T][kdim] bf16, dw = dz^T x [n][kdim] bf16, dbias = sum_t dz float32 [n].
- *   x is bf16, or MXFP8 codes with x_scales (x_dtype MOE_DT_MXFP8, kdim a multiple of 32): the
- *   8-bit checkpoint stands for x everywhere, also in z.  dy bf16 [T][n].  z is recomputed when fn is not
- *   MOE_FN_NONE; dz is rounded to bf16 for the two products (the matrix cores' operand type) and not for
- *   dbias.  Any of dx, dw, dbias may be NULL (not wanted), not all.  The residual's gradient is dy.
+ *   dx = dz W [T][kdim] of dx_dtype (bf16 or float32), dw = dz^T x [n][kdim] bf16,
+ *   dbias = sum_t dz float32 [n].  dy bf16 [T][n].
+ *   x is bf16 or float32, or MXFP8 codes with x_scales (x_dtype MOE_DT_MXFP8, kdim a multiple of 32):
+ *   the 8-bit checkpoint stands for x everywhere, also in z.  z is recomputed when fn is not
+ *   MOE_FN_NONE.  For dx and dw, dz is rounded to bf16 (the matrix cores' operand type) when T > 64
+ *   and kept as two bf16 terms up to there; dbias sums the unrounded values.  Any of dx, dw, dbias
+ *   may be NULL (not wanted), not all.  The residual's gradient is dy.
  *   x may be NULL when fn is MOE_FN_NONE and dw is NULL; w when fn is MOE_FN_NONE and dx is NULL.
  *   bias is read only when fn is not MOE_FN_NONE.  y_dtype is ignored.
  *   With T == 0 dw and dbias are written as zeros.
  */
 typedef struct {
     int32_t T, n, kdim;
-    int32_t fn;           /* MOE_FN_*                                   */
-    int32_t x_dtype;      /* MOE_DT_*: type of x                        */
-    int32_t y_dtype;      /* MOE_DT_BF16 or MOE_DT_F32: type of y       */
+    int32_t fn;           /* MOE_FN_*                                        */
+    int32_t x_dtype;      /* MOE_DT_*: type of x (MXFP8: backward only)      */
+    int32_t y_dtype;      /* MOE_DT_BF16 or MOE_DT_F32: type of y (forward)  */
+    int32_t dx_dtype;     /* MOE_DT_BF16 or MOE_DT_F32: type of dx (backward) */
 } moe_linear_desc;
 moe_status moe_dense_linear(const moe_linear_desc *desc, const void *x, const void *w, const float *bias,
                             const void *residual, void *y, void *ws, size_t ws_bytes, moe_stream stream);
@@ -425,22 +428,24 @@ size_t moe_dense_linear_backward_workspace(const moe_linear_desc *desc);
  *   x bf16 [T][d_model]; w_gate, w_up [d_ff][d_model]; b_gate, b_up [d_ff] or NULL;
  *   h [T][d_ff] of h_dtype (bf16 or float32); pre: bf16 [2][T][d_ff] (g, then u, rounded) or NULL.
  *   With moe_dense_linear as its down projection this is a whole SwiGLU / GEGLU / ReGLU block.
- * moe_dense_gateup_backward -- from dh [T][d_ff] bf16:
+ * moe_dense_gateup_backward -- from dh [T][d_ff] of dh_dtype (bf16 or float32):
  *   dg = dh u f'(g), du = dh f(g);  dx = dg w_gate + du w_up [T][d_model] bf16;
  *   dw_gate = dg^T x, dw_up = du^T x [d_ff][d_model] bf16; db_gate, db_up: column sums, float32.
  *   pre == NULL: g and u are recomputed from x in the product kernel, which forms dg and du in
  *   its epilogue; pre given: they are read (b_gate and b_up are not).  x is bf16 or the MXFP8
  *   checkpoint with x_scales (x_dtype, d_model a multiple of 32); it may be NULL when pre is given and
- *   dw_gate is NULL.  h: bf16 [T][d_ff] or NULL, recomputed for the down projection's weight gradient.
- *   dg and du are rounded to bf16 for the products and not for the bias gradients.  dw_gate and
- *   dw_up come together or not at all, as do db_gate and db_up; dx, dw_*, db_* and h may be NULL, not all.
+ *   dw_gate is NULL.  h: [T][d_ff] of h_dtype or NULL, recomputed for the down projection's weight
+ *   gradient.  For dx and dw_*, dg and du are rounded to bf16 when T > 64 and kept as two bf16 terms
+ *   up to there; the bias gradients sum the unrounded values.  dw_gate and dw_up come together or
+ *   not at all, as do db_gate and db_up; dx, dw_*, db_* and h may be NULL, not all.
  *   With T == 0 the weight and bias gradients are written as zeros.
  */
 typedef struct {
     int32_t T, d_model, d_ff;
     int32_t fn;           /* MOE_FN_*                                   */
     int32_t x_dtype;      /* MOE_DT_BF16, or MOE_DT_MXFP8 (backward)    */
-    int32_t h_dtype;      /* MOE_DT_BF16 or MOE_DT_F32 (forward)        */
+    int32_t h_dtype;      /* MOE_DT_BF16 or MOE_DT_F32: type of h       */
+    int32_t dh_dtype;     /* MOE_DT_BF16 or MOE_DT_F32: type of dh      */
 } moe_gateup_desc;
 moe_status moe_dense_gateup(const moe_gateup_desc *desc, const void *x, const void *w_gate, const void *w_up,
                             const float *b_gate, const float *b_up, void *h, void *pre, void *ws, size_t ws_bytes,

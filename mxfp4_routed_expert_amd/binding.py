@@ -56,11 +56,13 @@ class ExpertWeightsC(ctypes.Structure):
 
 
 class LinearDesc(ctypes.Structure):
-    _fields_ = [("T", _i32), ("n", _i32), ("kdim", _i32), ("fn", _i32), ("x_dtype", _i32), ("y_dtype", _i32)]
+    _fields_ = [("T", _i32), ("n", _i32), ("kdim", _i32), ("fn", _i32), ("x_dtype", _i32), ("y_dtype", _i32),
+                ("dx_dtype", _i32)]
 
 
 class GateupDesc(ctypes.Structure):
-    _fields_ = [("T", _i32), ("d_model", _i32), ("d_ff", _i32), ("fn", _i32), ("x_dtype", _i32), ("h_dtype", _i32)]
+    _fields_ = [("T", _i32), ("d_model", _i32), ("d_ff", _i32), ("fn", _i32), ("x_dtype", _i32), ("h_dtype", _i32),
+                ("dh_dtype", _i32)]
 
 
 def _sig(name, res, *args):
@@ -619,19 +621,19 @@ def _dense_plan(kind, *sizes):
 
 
 def moe_dense_linear_workspace(T, n, kdim, act_fn="none", x_dtype=torch.bfloat16, out_dtype=torch.bfloat16):
-    return _dense_plan("linear", T, n, kdim, _act_fn(act_fn), DT[x_dtype], DT[out_dtype])[1]
+    return _dense_plan("linear", T, n, kdim, _act_fn(act_fn), DT[x_dtype], DT[out_dtype], 0)[1]
 
 
-def moe_dense_linear_backward_workspace(T, n, kdim, act_fn="none", mxfp8=False):
-    return _dense_plan("linear_backward", T, n, kdim, _act_fn(act_fn), DT_MXFP8 if mxfp8 else 0, 0)[1]
+def moe_dense_linear_backward_workspace(T, n, kdim, act_fn="none", x_dtype=torch.bfloat16, mxfp8=False):
+    return _dense_plan("linear_backward", T, n, kdim, _act_fn(act_fn), DT_MXFP8 if mxfp8 else DT[x_dtype], 0, 0)[1]
 
 
 def moe_dense_gateup_workspace(T, d_model, d_ff, act_fn="silu", out_dtype=torch.bfloat16):
-    return _dense_plan("gateup", T, d_model, d_ff, _act_fn(act_fn), 0, DT[out_dtype])[1]
+    return _dense_plan("gateup", T, d_model, d_ff, _act_fn(act_fn), 0, DT[out_dtype], 0)[1]
 
 
 def moe_dense_gateup_backward_workspace(T, d_model, d_ff, act_fn="silu", mxfp8=False):
-    return _dense_plan("gateup_backward", T, d_model, d_ff, _act_fn(act_fn), DT_MXFP8 if mxfp8 else 0, 0)[1]
+    return _dense_plan("gateup_backward", T, d_model, d_ff, _act_fn(act_fn), DT_MXFP8 if mxfp8 else 0, 0, 0)[1]
 
 
 def _ws_for(ws, need, dev):
@@ -655,7 +657,7 @@ def moe_dense_linear(x, w, bias=None, act_fn="none", residual=None, out=None, ou
     dev = x.device
     _operands(dev, (x, tuple(DT), "x", None), (w, torch.bfloat16, "w", (n, kdim)), (bias, torch.float32, "bias", (n,)),
               (residual, dt, "residual", (T, n)), (out, dt, "out", (T, n)))
-    d, need = _dense_plan("linear", T, n, kdim, _act_fn(act_fn), DT[x.dtype], DT[dt])
+    d, need = _dense_plan("linear", T, n, kdim, _act_fn(act_fn), DT[x.dtype], DT[dt], 0)
     with _on(x):
         y = out if out is not None else torch.empty((T, n), dtype=dt, device=dev)
         ws, nws = _ws_for(ws, need, dev)
@@ -671,31 +673,34 @@ def _wanted(want, names):
     return [n in want for n in names]
 
 
-def _saved_input(x, x_scales, T, width, what):
-    """(x_dtype, operand rows) of an input kept as bf16 or as MXFP8 codes with their scales."""
+def _saved_input(x, x_scales, T, width, types):
+    """(x_dtype, operand rows) of an input kept as it is (one of `types`) or as MXFP8 codes with their scales."""
     mx = x_scales is not None
-    return (DT_MXFP8 if mx else 0), ((x, torch.uint8 if mx else torch.bfloat16, what, (T, width)),
-                                     (x_scales, torch.uint8, "x_scales", (T, width // 32)))
+    dt = DT_MXFP8 if mx else (DT.get(x.dtype, 0) if isinstance(x, torch.Tensor) else 0)
+    return dt, ((x, torch.uint8 if mx else types, "x", (T, width)), (x_scales, torch.uint8, "x_scales", (T, width // 32)))
 
 
 def moe_dense_linear_backward(dy, x, w, bias=None, act_fn="none", x_scales=None, want=("dx", "dw", "dbias"), out=None,
-                              ws=None):
-    """Gradients of moe_dense_linear at dy (bf16 [T][n]): (dx bf16 [T][kdim], dw bf16 [n][kdim], dbias float32 [n]), None
-    for what `want` does not name.  x: bf16, or the codes of moe_mxfp8_quantize with their x_scales.
-    out: the three results' tensors (None where not wanted)."""
+                              dx_dtype=None, ws=None):
+    """Gradients of moe_dense_linear at dy (bf16 [T][n]): (dx [T][kdim] of dx_dtype (bf16 when None, or float32), dw bf16
+    [n][kdim], dbias float32 [n]), None for what `want` does not name.  x: bf16 or float32, or the codes of
+    moe_mxfp8_quantize with their x_scales.  out: the three results' tensors (None where not wanted)."""
     T, n = _matrix(dy, "dy")
     kdim = _matrix(w, "w")[1]
     fx, fw, fb = _wanted(want, ("dx", "dw", "dbias"))
-    xdt, xitems = _saved_input(x, x_scales, T, kdim, "x")
+    xdt, xitems = _saved_input(x, x_scales, T, kdim, tuple(DT))
     dev = dy.device
     ox, ow, ob = out if out is not None else (None, None, None)
     bf = torch.bfloat16
+    xt = ox.dtype if ox is not None else (dx_dtype or bf)
+    if xt not in DT:
+        raise TypeError(f"dx must be bfloat16 or float32 (got {xt})")
     _operands(dev, (dy, bf, "dy", None), *xitems, (w, bf, "w", (n, kdim)), (bias, torch.float32, "bias", (n,)),
-              (ox, bf, "dx", (T, kdim)), (ow, bf, "dw", (n, kdim)), (ob, torch.float32, "dbias", (n,)))
-    d, need = _dense_plan("linear_backward", T, n, kdim, _act_fn(act_fn), xdt, 0)
+              (ox, xt, "dx", (T, kdim)), (ow, bf, "dw", (n, kdim)), (ob, torch.float32, "dbias", (n,)))
+    d, need = _dense_plan("linear_backward", T, n, kdim, _act_fn(act_fn), xdt, 0, DT[xt])
     with _on(dy):
         e = lambda o, on, shape, dt: None if not on else (o if o is not None else torch.empty(shape, dtype=dt, device=dev))
-        dx, dw, db = e(ox, fx, (T, kdim), bf), e(ow, fw, (n, kdim), bf), e(ob, fb, (n,), torch.float32)
+        dx, dw, db = e(ox, fx, (T, kdim), xt), e(ow, fw, (n, kdim), bf), e(ob, fb, (n,), torch.float32)
         ws, nws = _ws_for(ws, need, dev)
         check(lib.moe_dense_linear_backward(ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(x_scales), _ptr(w), _ptr(bias),
                                             _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nws, _stream()))
@@ -729,25 +734,29 @@ def moe_dense_gateup(x, w_gate, w_up, b_gate=None, b_up=None, act_fn="silu", out
 
 
 def moe_dense_gateup_backward(dh, x, w_gate, w_up, b_gate=None, b_up=None, act_fn="silu", x_scales=None, pre=None,
-                              want=("dx", "dw", "db"), want_h=False, out=None, ws=None):
-    """Gradients of moe_dense_gateup at dh (bf16 [T][d_ff]): (dx, dw_gate, dw_up, db_gate, db_up, h), None for what was
-    not asked for; h (bf16) is the forward result again, for the down projection's weight gradient.  x: bf16, or MXFP8
+                              want=("dx", "dw", "db"), want_h=False, h_dtype=None, out=None, ws=None):
+    """Gradients of moe_dense_gateup at dh (bf16 or float32 [T][d_ff]): (dx, dw_gate, dw_up, db_gate, db_up, h), None for
+    what was not asked for; the weights' gradients and dx are bf16, the biases' float32.  h (of h_dtype, bf16 when None,
+    or float32) is the forward result again, for the down projection's weight gradient.  x: bf16, or MXFP8
     codes with x_scales; pre: the forward call's pre-activations (recomputed from x when None).  out: the six results'
     tensors."""
     T, f = _matrix(dh, "dh")
     dm = _matrix(w_gate, "w_gate")[1]
     fx, fw, fb = _wanted(want, ("dx", "dw", "db")) if want or not want_h else (False, False, False)
-    xdt, xitems = _saved_input(x, x_scales, T, dm, "x")
+    xdt, xitems = _saved_input(x, x_scales, T, dm, torch.bfloat16)
     dev = dh.device
     bf, f32 = torch.bfloat16, torch.float32
     o = out if out is not None else (None,) * 6
+    ht = o[5].dtype if o[5] is not None else (h_dtype or bf)
+    if ht not in DT:
+        raise TypeError(f"h must be bfloat16 or float32 (got {ht})")
     names = ("dx", "dw_gate", "dw_up", "db_gate", "db_up", "h")
     shapes = ((T, dm), (f, dm), (f, dm), (f,), (f,), (T, f))
-    types = (bf, bf, bf, f32, f32, bf)
-    _operands(dev, (dh, bf, "dh", None), *xitems, (w_gate, bf, "w_gate", (f, dm)), (w_up, bf, "w_up", (f, dm)),
+    types = (bf, bf, bf, f32, f32, ht)
+    _operands(dev, (dh, tuple(DT), "dh", None), *xitems, (w_gate, bf, "w_gate", (f, dm)), (w_up, bf, "w_up", (f, dm)),
               (b_gate, f32, "b_gate", (f,)), (b_up, f32, "b_up", (f,)), (pre, bf, "pre", (2, T, f)),
               *((t, dt, nm, sh) for t, dt, nm, sh in zip(o, types, names, shapes)))
-    d, need = _dense_plan("gateup_backward", T, dm, f, _act_fn(act_fn), xdt, 0)
+    d, need = _dense_plan("gateup_backward", T, dm, f, _act_fn(act_fn), xdt, DT[ht], DT[dh.dtype])
     with _on(dh):
         r = [None if not on else (t if t is not None else torch.empty(sh, dtype=dt, device=dev))
              for t, dt, sh, on in zip(o, types, shapes, (fx, fw, fw, fb, fb, want_h))]

@@ -140,14 +140,32 @@ struct EpiGate {
     }
 };
 
-// dz = dy * f'(z + bias), rounded to bf16 for the two gradient products; the bias gradient sums
-// the unrounded values.  dz rows are ldz >= C wide (a multiple of 8); the columns past C are
+// Up to this many tokens a value that feeds a product is kept as several bf16 terms (its rounding, and
+// the rounding of what is left) instead of one: the products are then bound by the weights' bytes,
+// and the terms ride along as further rows of the same tile.  Beyond it dz (dg, du) is one bf16
+// value, the operand type of the matrix cores: one rounding of 2^-8 at most per value, and the
+// products cost half.
+constexpr int kTermTokens = 64;
+
+// What a bf16 rounding of v leaves (0 where the rounding is infinite or NaN).
+MOE_DEV f32x4 low_terms(const f32x4 v) {
+    f32x4 r;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const float h = (float)(__bf16)v[q];
+        r[q] = fabsf(h) <= 3.4028234e38f ? v[q] - h : 0.0f;
+    }
+    return r;
+}
+
+// dz = dy * f'(z + bias), rounded to bf16 for the two gradient products (and its low terms, when
+// lo is given); the bias gradient sums the unrounded values.  dz rows are ldz >= C wide (a multiple of 8); the columns past C are
 // written as zeros, so the products may read whole 16-byte chunks.
 struct EpiLinearBwd {
     static constexpr bool kPair = false, kColSum = true;
     const float *bias;
     const uint16_t *dy;
-    uint16_t *dz;
+    uint16_t *dz, *lo;    // lo: NULL, or the low terms' rows
     int C, ldz, fn;
     float *cs;            // column-sum partials [..][csld] or NULL
     int csld;
@@ -171,29 +189,37 @@ struct EpiLinearBwd {
             act_fd(fn, a[q], f, d);
             ca[q] = c + q < C ? g[q] * d : 0.0f;
         }
+        const bool tail = c + 4 >= C && c + 4 < ldz;
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
         store4_bf16(dz + (size_t)r * ldz + c, ca);
-        if (c + 4 >= C && c + 4 < ldz) store4_bf16(dz + (size_t)r * ldz + c + 4, f32x4{0.f, 0.f, 0.f, 0.f});
+        if (tail) store4_bf16(dz + (size_t)r * ldz + c + 4, zero);
+        if (lo) {
+            store4_bf16(lo + (size_t)r * ldz + c, low_terms(ca));
+            if (tail) store4_bf16(lo + (size_t)r * ldz + c + 4, zero);
+        }
     }
 };
 
 // dg = dh * u * f'(g), du = dh * f(g), rounded to bf16 into [R][2][C] (one row of 2C values, so
-// the weight-gradient product sees one matrix); h = f(g) * u when asked for.  C is a multiple of 8.
+// the weight-gradient product sees one matrix; low terms as above); h = f(g) * u when asked for.
+// C is a multiple of 8.
 struct EpiGateBwd {
     static constexpr bool kPair = true, kColSum = true;
     const float *bg, *bu;
-    const uint16_t *dh;
-    uint16_t *dgu;
-    uint16_t *h;          // [R][C] or NULL
-    int C, fn;
+    const void *dh;       // bf16 or float32
+    uint16_t *dgu, *lo;
+    void *h;              // [R][C] or NULL
+    int C, fn, dh_f32, h_f32;
     float *cs;            // column-sum partials [..][csld], csld = 2C, or NULL
     int csld;
     MOE_DEV void apply(int r, int c, f32x4 a, f32x4 b, f32x4 &ca, f32x4 &cb) const {
-        const size_t o = (size_t)r * C + c;
         if (bg) a += *(const f32x4 *)(bg + c);
         if (bu) b += *(const f32x4 *)(bu + c);
-        grads(r, c, load4_bf16(dh + o), a, b, ca, cb);
+        grads(r, c, a, b, ca, cb);
     }
-    MOE_DEV void grads(int r, int c, f32x4 d, f32x4 g, f32x4 u, f32x4 &ca, f32x4 &cb) const {
+    MOE_DEV void grads(int r, int c, f32x4 g, f32x4 u, f32x4 &ca, f32x4 &cb) const {
+        const size_t o = (size_t)r * C + c;
+        const f32x4 d = dh_f32 ? *(const f32x4 *)((const float *)dh + o) : load4_bf16((const uint16_t *)dh + o);
         f32x4 hv;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -205,20 +231,29 @@ struct EpiGateBwd {
         }
         store4_bf16(dgu + (size_t)r * 2 * C + c, ca);
         store4_bf16(dgu + (size_t)r * 2 * C + C + c, cb);
-        if (h) store4_bf16(h + (size_t)r * C + c, hv);
+        if (lo) {
+            store4_bf16(lo + (size_t)r * 2 * C + c, low_terms(ca));
+            store4_bf16(lo + (size_t)r * 2 * C + C + c, low_terms(cb));
+        }
+        if (h) {
+            if (h_f32) *(f32x4 *)((float *)h + o) = hv;
+            else store4_bf16((uint16_t *)h + o, hv);
+        }
     }
 };
 
-// Rounded product: rows below rows0 to out0, the others to out1 (the gate's and up's gradients).
+// The product itself: rows below rows0 to out0, the others to out1 (the gate's and up's gradients).
 // C is a multiple of 8.
 struct EpiStore {
     static constexpr bool kPair = false, kColSum = false;
-    uint16_t *out0, *out1;
-    int rows0, C;
+    void *out0, *out1;
+    int rows0, C, f32;
     float *cs = nullptr;
     MOE_DEV void apply(int r, int c, f32x4 a, f32x4, f32x4 &, f32x4 &) const {
-        uint16_t *p = r < rows0 ? out0 + (size_t)r * C : out1 + (size_t)(r - rows0) * C;
-        store4_bf16(p + c, a);
+        void *p = r < rows0 ? out0 : out1;
+        const size_t o = (size_t)(r < rows0 ? r : r - rows0) * C + c;
+        if (f32) *(f32x4 *)((float *)p + o) = a;
+        else store4_bf16((uint16_t *)p + o, a);
     }
 };
 
@@ -246,14 +281,16 @@ enum DenseForm { kFormNT = 0, kFormNN = 1, kFormTN = 2 };
 //   NN: rowop as NT,                      colop(c, k) = cp[s][k * ldc + c]
 //   TN: rowop(r, k) = rp[s][k * ldr + r], colop as NN
 // Pair (NT, one segment): cp[0] and cp[1] are two matrices of C rows, both products wanted.
-// Segments let one launch sum over the terms of a split float32 operand, or over gate and up.
+// Segments let one launch sum over the terms of a split operand, or over gate and up.  With
+// terms > 1 the rows operand holds R / terms output rows of each term, one term's rows after the
+// other's, and the results of a row's terms are added up (not for pairs).
 // Every row start is 16-byte aligned; K (contiguous operands) and the widths of strided operands
 // are multiples of 8.
 struct DenseProduct {
     const uint16_t *rp[3];
     const uint16_t *cp[3];
-    int nseg, K;
-    int R, C;
+    int nseg, terms, K;
+    int R, C;             // R: rows of the rows operand, all terms
     int ldr, ldc;
     int rcols;            // TN: readable columns of a row-operand row (>= R, a multiple of 8)
 };
@@ -266,8 +303,8 @@ struct DensePlan {
     int steps;            // 64-value steps of the sum, all segments
     int cs_rows;          // column-sum partial rows the launch writes
 };
-DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg);
-size_t dense_plan_bytes(const DensePlan &pl, bool pair, int R, int C);   // partial results, 0 for split 1
+DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg, int terms = 1);
+size_t dense_plan_bytes(const DensePlan &pl, bool pair, int R, int C, int terms = 1);   // partial results
 
 moe_status dense_linear_product(const DenseProduct &p, const DensePlan &pl, const EpiLinear &e, float *part, hipStream_t s);
 moe_status dense_gate_product(const DenseProduct &p, const DensePlan &pl, const EpiGate &e, float *part, hipStream_t s);
@@ -280,7 +317,7 @@ moe_status dense_tn_product(const DenseProduct &p, const DensePlan &pl, const Ep
 
 // Sum the parts of a split product and run the epilogue on the sums (dense_aux.hip).
 template <class Epi>
-moe_status dense_finish(const DensePlan &pl, const Epi &e, const float *part, int R, int C, hipStream_t s);
+moe_status dense_finish(int parts, const Epi &e, const float *part, int R, int C, hipStream_t s);
 constexpr int kFinishRows = 2;    // rows per workgroup of the finish and saved-activation kernels
 
 // out[c] = sum over rows of part[row][c] (column-sum partials), in row order.

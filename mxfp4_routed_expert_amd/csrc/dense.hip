@@ -18,7 +18,7 @@ constexpr int kMaxSplit = 16;
 
 // The tile shape and split with the least estimated time: rounds of workgroups over the CUs times
 // their steps, plus the traffic of the partial results and the launch that sums them.
-DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg) {
+DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg, int terms) {
     DensePlan best = {};
     double best_t = 1e30;
     const int steps = (K + 63) / 64 * nseg;
@@ -36,19 +36,19 @@ DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg) {
             const int64_t last = (wgs - (rounds - 1) * slots + kCUs - 1) / kCUs;
             const double load = (double)(rounds - 1) + (0.35 + 0.65 * (double)last / t.per_cu);
             double us = load * (((steps + split - 1) / split) * t.step + t.tile);
-            if (split > 1) us += 3.0 + (double)R * C * mats * 4.0 * split * 2.0 / 4.0e6;
+            if (split * terms > 1) us += 3.0 + (double)R * C * mats * 4.0 * split * 2.0 / 4.0e6;
             if (us < best_t) {
                 best_t = us;
                 best = DensePlan{cfg, split, tr, tc, steps,
-                                 split > 1 ? (R + kFinishRows - 1) / kFinishRows : tr * t.wr};
+                                 split * terms > 1 ? (R / terms + kFinishRows - 1) / kFinishRows : tr * t.wr};
             }
         }
     }
     return best;
 }
 
-size_t dense_plan_bytes(const DensePlan &pl, bool pair, int R, int C) {
-    if (pl.split == 1) return 0;
+size_t dense_plan_bytes(const DensePlan &pl, bool pair, int R, int C, int terms) {
+    if (pl.split * terms == 1) return 0;
     return (size_t)pl.split * (pair ? 2 : 1) * R * ((C + 3) & ~3) * sizeof(float);
 }
 
@@ -91,20 +91,21 @@ moe_status check_linear(const char *who, const moe_linear_desc *d, bool backward
                 "%s: need T >= 0, n > 0, kdim > 0 and a multiple of 8 (T=%d n=%d kdim=%d)", who, d->T, d->n, d->kdim);
     MOE_REQUIRE(fn_ok(d->fn), "%s: unknown activation %d", who, d->fn);
     if (backward) {
-        MOE_REQUIRE(d->x_dtype == MOE_DT_BF16 || d->x_dtype == MOE_DT_MXFP8, "%s: x_dtype %d is neither bf16 nor MXFP8", who,
-                    d->x_dtype);
+        MOE_REQUIRE(d->x_dtype >= MOE_DT_BF16 && d->x_dtype <= MOE_DT_MXFP8, "%s: unknown x_dtype %d", who, d->x_dtype);
+        MOE_REQUIRE(d->dx_dtype == MOE_DT_BF16 || d->dx_dtype == MOE_DT_F32, "%s: unknown dx_dtype %d", who, d->dx_dtype);
         MOE_REQUIRE(d->x_dtype != MOE_DT_MXFP8 || d->kdim % 32 == 0, "%s: MXFP8 kdim = %d is not a multiple of 32", who,
                     d->kdim);
     } else {
         MOE_REQUIRE(d->x_dtype == MOE_DT_BF16 || d->x_dtype == MOE_DT_F32, "%s: unknown x_dtype %d", who, d->x_dtype);
         MOE_REQUIRE(d->y_dtype == MOE_DT_BF16 || d->y_dtype == MOE_DT_F32, "%s: unknown y_dtype %d", who, d->y_dtype);
     }
-    MOE_REQUIRE(fits31(d->T, d->n + 8) && fits31(d->n, d->kdim) && fits31(d->T, d->kdim), "%s: sizes overflow int32", who);
+    MOE_REQUIRE(fits31(d->T, (int64_t)d->n + 8) && fits31(d->n, d->kdim) && fits31(d->T, d->kdim), "%s: sizes overflow int32", who);
     return MOE_OK;
 }
 
 struct LinearWs {
     DensePlan plan;
+    int terms, nseg;
     uint16_t *planes;
     float *part;
     size_t bytes;
@@ -114,15 +115,22 @@ LinearWs linear_ws(const moe_linear_desc *d, void *base) {
     if (d->T <= kGemvTokens) return w;
     const bool f32 = d->x_dtype == MOE_DT_F32;
     Carve c{(char *)base};
-    w.plan = dense_plan(kFormNT, false, d->T, d->n, d->kdim, f32 ? 3 : 1);
+    w.terms = f32 && d->T <= kTermTokens ? 3 : 1;
+    w.nseg = f32 && w.terms == 1 ? 3 : 1;
+    w.plan = dense_plan(kFormNT, false, d->T * w.terms, d->n, d->kdim, w.nseg, w.terms);
     w.planes = c.take<uint16_t>(f32 ? (size_t)3 * d->T * d->kdim * 2 : 0);
-    w.part = c.take<float>(dense_plan_bytes(w.plan, false, d->T, d->n));
+    w.part = c.take<float>(dense_plan_bytes(w.plan, false, d->T * w.terms, d->n, w.terms));
     w.bytes = c.at;
     return w;
 }
 
+// The sums of a linear layer's backward pass.  Up to kTermTokens tokens dz = dy f' is kept as two terms;
+// a float32 x is three terms for z and its two leading ones (2^-16) for dw, whose result is bf16.
 struct LinearBwdWs {
     DensePlan pz, px, pw;
+    int zterms, zseg;            // recomputed z: x's terms as rows or as segments
+    int dterms;                  // terms of dz
+    int wseg;                    // (dz term, x term) products in dw
     uint16_t *x, *dz;
     float *cs, *part;
     int ldz, csld, cs_rows;
@@ -132,19 +140,24 @@ struct LinearBwdWs {
 LinearBwdWs linear_bwd_ws(const moe_linear_desc *d, void *base) {
     LinearBwdWs w = {};
     Carve c{(char *)base};
-    const bool act = d->fn != MOE_FN_NONE;
-    w.ldz = (d->n + 7) & ~7;
+    const int T = d->T, n = d->n, k = d->kdim;
+    const bool act = d->fn != MOE_FN_NONE, f32 = d->x_dtype == MOE_DT_F32, few = T <= kTermTokens;
+    w.ldz = (n + 7) & ~7;
     w.csld = w.ldz;
-    w.own_dz = act || w.ldz != d->n;       // dy itself serves as dz otherwise
-    w.pz = dense_plan(kFormNT, false, d->T, d->n, d->kdim, 1);
-    w.px = dense_plan(kFormNN, false, d->T, d->kdim, d->n, 1);
-    w.pw = dense_plan(kFormTN, false, d->n, d->kdim, d->T, 1);
-    w.cs_rows = act ? w.pz.cs_rows : (d->T + kColRows - 1) / kColRows;
-    w.x = c.take<uint16_t>(d->x_dtype == MOE_DT_MXFP8 ? (size_t)d->T * d->kdim * 2 : 0);
-    w.dz = c.take<uint16_t>(w.own_dz ? (size_t)d->T * w.ldz * 2 : 0);
+    w.own_dz = act || w.ldz != n;          // dy itself serves as dz otherwise
+    w.zterms = f32 && few ? 3 : 1;
+    w.zseg = f32 && !few ? 3 : 1;
+    w.dterms = act && few ? 2 : 1;
+    w.wseg = (f32 ? 2 : 1) + (w.dterms - 1);
+    w.pz = dense_plan(kFormNT, false, T * w.zterms, n, k, w.zseg, w.zterms);
+    w.px = dense_plan(kFormNN, false, T * w.dterms, k, n, 1, w.dterms);
+    w.pw = dense_plan(kFormTN, false, n, k, T, w.wseg);
+    w.cs_rows = act ? w.pz.cs_rows : (T + kColRows - 1) / kColRows;
+    w.x = c.take<uint16_t>(f32 ? (size_t)3 * T * k * 2 : (d->x_dtype == MOE_DT_MXFP8 ? (size_t)T * k * 2 : 0));
+    w.dz = c.take<uint16_t>(w.own_dz ? (size_t)w.dterms * T * w.ldz * 2 : 0);
     w.cs = c.take<float>((size_t)w.cs_rows * w.csld * 4);
-    size_t part = act ? dense_plan_bytes(w.pz, false, d->T, d->n) : 0;
-    const size_t bx = dense_plan_bytes(w.px, false, d->T, d->kdim), bw = dense_plan_bytes(w.pw, false, d->n, d->kdim);
+    size_t part = act ? dense_plan_bytes(w.pz, false, T * w.zterms, n, w.zterms) : 0;
+    const size_t bx = dense_plan_bytes(w.px, false, T * w.dterms, k, w.dterms), bw = dense_plan_bytes(w.pw, false, n, k);
     part = part > bx ? part : bx;
     part = part > bw ? part : bw;
     w.part = c.take<float>(part);
@@ -163,13 +176,14 @@ moe_status check_gateup(const char *who, const moe_gateup_desc *d, bool backward
     if (backward) {
         MOE_REQUIRE(d->x_dtype == MOE_DT_BF16 || d->x_dtype == MOE_DT_MXFP8, "%s: x_dtype %d is neither bf16 nor MXFP8", who,
                     d->x_dtype);
+        MOE_REQUIRE(d->dh_dtype == MOE_DT_BF16 || d->dh_dtype == MOE_DT_F32, "%s: unknown dh_dtype %d", who, d->dh_dtype);
         MOE_REQUIRE(d->x_dtype != MOE_DT_MXFP8 || d->d_model % 32 == 0, "%s: MXFP8 d_model = %d is not a multiple of 32", who,
                     d->d_model);
     } else {
         MOE_REQUIRE(d->x_dtype == MOE_DT_BF16, "%s: x must be bf16 (x_dtype %d)", who, d->x_dtype);
-        MOE_REQUIRE(d->h_dtype == MOE_DT_BF16 || d->h_dtype == MOE_DT_F32, "%s: unknown h_dtype %d", who, d->h_dtype);
     }
-    MOE_REQUIRE(d->d_ff < INT32_MAX / 2 && fits31(d->T, 2 * d->d_ff) && fits31(d->d_model, 2 * d->d_ff) &&
+    MOE_REQUIRE(d->h_dtype == MOE_DT_BF16 || d->h_dtype == MOE_DT_F32, "%s: unknown h_dtype %d", who, d->h_dtype);
+    MOE_REQUIRE(fits31(d->T, 2 * (int64_t)d->d_ff) && fits31(d->d_model, 2 * (int64_t)d->d_ff) &&
                     fits31(d->T, d->d_model),
                 "%s: sizes overflow int32", who);
     return MOE_OK;
@@ -192,6 +206,7 @@ GateWs gate_ws(const moe_gateup_desc *d, void *base) {
 
 struct GateBwdWs {
     DensePlan pg, px, pw;
+    int terms;                   // of dg and du
     uint16_t *x, *dgu;
     float *cs, *part;
     int cs_rows;                 // with recomputed pre-activations
@@ -203,15 +218,17 @@ GateBwdWs gate_bwd_ws(const moe_gateup_desc *d, void *base) {
     Carve c{(char *)base};
     const int f = d->d_ff;
     w.pg = dense_plan(kFormNT, true, d->T, f, d->d_model, 1);
-    w.px = dense_plan(kFormNN, false, d->T, d->d_model, f, 2);
-    w.pw = dense_plan(kFormTN, false, 2 * f, d->d_model, d->T, 1);
+    w.terms = d->T <= kTermTokens ? 2 : 1;
+    const int xr = d->T * w.terms;
+    w.px = dense_plan(kFormNN, false, xr, d->d_model, f, 2, w.terms);
+    w.pw = dense_plan(kFormTN, false, 2 * f, d->d_model, d->T, w.terms);
     w.cs_rows = w.pg.cs_rows;
     w.cs_rows_saved = (d->T + kFinishRows - 1) / kFinishRows;
     w.x = c.take<uint16_t>(d->x_dtype == MOE_DT_MXFP8 ? (size_t)d->T * d->d_model * 2 : 0);
-    w.dgu = c.take<uint16_t>((size_t)d->T * 2 * f * 2);
+    w.dgu = c.take<uint16_t>((size_t)xr * 2 * f * 2);
     w.cs = c.take<float>((size_t)(w.cs_rows > w.cs_rows_saved ? w.cs_rows : w.cs_rows_saved) * 2 * f * 4);
     size_t part = dense_plan_bytes(w.pg, true, d->T, f);
-    const size_t bx = dense_plan_bytes(w.px, false, d->T, d->d_model), bw = dense_plan_bytes(w.pw, false, 2 * f, d->d_model);
+    const size_t bx = dense_plan_bytes(w.px, false, xr, d->d_model, w.terms), bw = dense_plan_bytes(w.pw, false, 2 * f, d->d_model);
     part = part > bx ? part : bx;
     part = part > bw ? part : bw;
     w.part = c.take<float>(part);
@@ -250,13 +267,14 @@ extern "C" moe_status moe_dense_linear(const moe_linear_desc *d, const void *x, 
     const size_t plane = (size_t)d->T * d->kdim;
     if (f32) MOE_TRY(dense_split3((const float *)x, b.planes, plane, s));
     DenseProduct p = {};
-    p.nseg = f32 ? 3 : 1;
+    p.nseg = b.nseg;
+    p.terms = b.terms;
     for (int i = 0; i < p.nseg; ++i) {
         p.rp[i] = f32 ? b.planes + i * plane : (const uint16_t *)x;
         p.cp[i] = (const uint16_t *)w;
     }
     p.K = p.ldr = p.ldc = d->kdim;
-    p.R = d->T;
+    p.R = d->T * b.terms;
     p.C = d->n;
     return dense_linear_product(p, b.plan, e, b.part, s);
 }
@@ -282,24 +300,32 @@ extern "C" moe_status moe_dense_linear_backward(const moe_linear_desc *d, const 
     MOE_TRY(check_ws("moe_dense_linear_backward", ws, ws_bytes, b.bytes));
     hipStream_t s = (hipStream_t)stream;
     const int T = d->T, n = d->n, k = d->kdim;
+    const bool f32 = d->x_dtype == MOE_DT_F32;
+    const size_t xplane = f32 ? (size_t)T * k : 0;
     const uint16_t *xb = (const uint16_t *)x;
-    if (T > 0 && mx && need_x) {
-        MOE_TRY(mxfp8_dequant_launch((size_t)T, k, (const uint8_t *)x, x_scales, b.x, false, s));
+    if (T > 0 && need_x && (mx || f32)) {
+        if (mx) MOE_TRY(mxfp8_dequant_launch((size_t)T, k, (const uint8_t *)x, x_scales, b.x, false, s));
+        else MOE_TRY(dense_split3((const float *)x, b.x, xplane, s));
         xb = b.x;
     }
     const uint16_t *dz = (const uint16_t *)dy;
+    const size_t dzplane = (size_t)T * b.ldz;
     if (T > 0 && act) {
         DenseProduct p = {};
-        p.nseg = 1;
-        p.rp[0] = xb;
-        p.cp[0] = (const uint16_t *)w;
+        p.nseg = b.zseg;
+        p.terms = b.zterms;
+        for (int i = 0; i < p.nseg; ++i) {
+            p.rp[i] = xb + i * xplane;
+            p.cp[i] = (const uint16_t *)w;
+        }
         p.K = p.ldr = p.ldc = k;
-        p.R = T;
+        p.R = T * b.zterms;
         p.C = n;
         EpiLinearBwd e;
         e.bias = bias;
         e.dy = dz;
         e.dz = b.dz;
+        e.lo = b.dterms > 1 ? b.dz + dzplane : nullptr;
         e.C = n;
         e.ldz = b.ldz;
         e.fn = d->fn;
@@ -318,25 +344,32 @@ extern "C" moe_status moe_dense_linear_backward(const moe_linear_desc *d, const 
     if (dx && T > 0) {
         DenseProduct p = {};
         p.nseg = 1;
+        p.terms = b.dterms;
         p.rp[0] = dz;
         p.cp[0] = (const uint16_t *)w;
         p.K = n;
         p.ldr = b.ldz;
         p.ldc = k;
-        p.R = T;
+        p.R = T * b.dterms;
         p.C = k;
         EpiStore e;
-        e.out0 = (uint16_t *)dx;
+        e.out0 = dx;
         e.out1 = nullptr;
         e.rows0 = T;
         e.C = k;
+        e.f32 = d->dx_dtype == MOE_DT_F32;
         MOE_TRY(dense_nn_product(p, b.px, e, b.part, s));
     }
     if (dw) {
+        // dz's leading term with x's one or two leading terms, then dz's low term with x's first
         DenseProduct p = {};
-        p.nseg = 1;
-        p.rp[0] = dz;
-        p.cp[0] = xb;
+        p.terms = 1;
+        p.nseg = b.wseg;
+        for (int i = 0; i < p.nseg; ++i) {
+            const bool lo = b.dterms > 1 && i == p.nseg - 1;
+            p.rp[i] = lo ? dz + dzplane : dz;
+            p.cp[i] = lo ? xb : xb + i * xplane;
+        }
         p.K = T;
         p.ldr = b.ldz;
         p.ldc = k;
@@ -344,10 +377,11 @@ extern "C" moe_status moe_dense_linear_backward(const moe_linear_desc *d, const 
         p.C = k;
         p.rcols = b.ldz;
         EpiStore e;
-        e.out0 = (uint16_t *)dw;
+        e.out0 = dw;
         e.out1 = nullptr;
         e.rows0 = n;
         e.C = k;
+        e.f32 = 0;
         MOE_TRY(dense_tn_product(p, b.pw, e, b.part, s));
     }
     return MOE_OK;
@@ -380,7 +414,7 @@ extern "C" moe_status moe_dense_gateup(const moe_gateup_desc *d, const void *x, 
     const uint16_t *xb = (const uint16_t *)x, *wg = (const uint16_t *)w_gate, *wu = (const uint16_t *)w_up;
     if (d->T <= kGemvTokens) return dense_gate_gemv(xb, wg, wu, d->T, d->d_ff, d->d_model, e, s);
     DenseProduct p = {};
-    p.nseg = 1;
+    p.nseg = p.terms = 1;
     p.rp[0] = xb;
     p.cp[0] = wg;
     p.cp[1] = wu;
@@ -424,9 +458,12 @@ extern "C" moe_status moe_dense_gateup_backward(const moe_gateup_desc *d, const 
         EpiGateBwd e;
         e.bg = b_gate;
         e.bu = b_up;
-        e.dh = (const uint16_t *)dh;
+        e.dh = dh;
         e.dgu = b.dgu;
-        e.h = (uint16_t *)h;
+        e.lo = b.terms > 1 ? b.dgu + (size_t)T * 2 * f : nullptr;
+        e.h = h;
+        e.dh_f32 = d->dh_dtype == MOE_DT_F32;
+        e.h_f32 = d->h_dtype == MOE_DT_F32;
         e.C = f;
         e.fn = d->fn;
         e.cs = db_gate ? b.cs : nullptr;
@@ -435,7 +472,7 @@ extern "C" moe_status moe_dense_gateup_backward(const moe_gateup_desc *d, const 
             MOE_TRY(dense_gate_bwd_saved(e, (const uint16_t *)pre, T, s));
         } else {
             DenseProduct p = {};
-            p.nseg = 1;
+            p.nseg = p.terms = 1;
             p.rp[0] = xb;
             p.cp[0] = wg;
             p.cp[1] = wu;
@@ -450,6 +487,7 @@ extern "C" moe_status moe_dense_gateup_backward(const moe_gateup_desc *d, const 
     if (dx && T > 0) {
         DenseProduct p = {};
         p.nseg = 2;
+        p.terms = b.terms;
         p.rp[0] = b.dgu;
         p.rp[1] = b.dgu + f;
         p.cp[0] = wg;
@@ -457,20 +495,24 @@ extern "C" moe_status moe_dense_gateup_backward(const moe_gateup_desc *d, const 
         p.K = f;
         p.ldr = 2 * f;
         p.ldc = dm;
-        p.R = T;
+        p.R = T * b.terms;
         p.C = dm;
         EpiStore e;
-        e.out0 = (uint16_t *)dx;
+        e.out0 = dx;
         e.out1 = nullptr;
         e.rows0 = T;
         e.C = dm;
+        e.f32 = 0;
         MOE_TRY(dense_nn_product(p, b.px, e, b.part, s));
     }
     if (dw_gate) {
         DenseProduct p = {};
-        p.nseg = 1;
-        p.rp[0] = b.dgu;
-        p.cp[0] = xb;
+        p.terms = 1;
+        p.nseg = b.terms;
+        for (int i = 0; i < p.nseg; ++i) {
+            p.rp[i] = b.dgu + (size_t)i * T * 2 * f;
+            p.cp[i] = xb;
+        }
         p.K = T;
         p.ldr = 2 * f;
         p.ldc = dm;
@@ -478,10 +520,11 @@ extern "C" moe_status moe_dense_gateup_backward(const moe_gateup_desc *d, const 
         p.C = dm;
         p.rcols = 2 * f;
         EpiStore e;
-        e.out0 = (uint16_t *)dw_gate;
-        e.out1 = (uint16_t *)dw_up;
+        e.out0 = dw_gate;
+        e.out1 = dw_up;
         e.rows0 = f;
         e.C = dm;
+        e.f32 = 0;
         MOE_TRY(dense_tn_product(p, b.pw, e, b.part, s));
     }
     return MOE_OK;

@@ -71,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void gate_bwd_saved_kernel(const uint16_t
         if (r >= R) break;
         const size_t o = (size_t)r * epi.C + c;
         f32x4 ca, cb;
-        epi.grads(r, c, load4_bf16(epi.dh + o), load4_bf16(pre + o), load4_bf16(pre + (size_t)R * epi.C + o), ca, cb);
+        epi.grads(r, c, load4_bf16(pre + o), load4_bf16(pre + (size_t)R * epi.C + o), ca, cb);
         sa += ca;
         sb += cb;
     }
@@ -167,15 +167,15 @@ __global__ __launch_bounds__(kThreads) void pad_rows_kernel(const uint16_t *__re
 }  // namespace
 
 template <class Epi>
-moe_status dense_finish(const DensePlan &pl, const Epi &e, const float *part, int R, int C, hipStream_t s) {
-    hipLaunchKernelGGL(dense_finish_kernel<Epi>, block_grid(R, kFinishRows, C), dim3(kThreads), 0, s, part, pl.split, R, C, (C + 3) & ~3, e);
+moe_status dense_finish(int parts, const Epi &e, const float *part, int R, int C, hipStream_t s) {
+    hipLaunchKernelGGL(dense_finish_kernel<Epi>, block_grid(R, kFinishRows, C), dim3(kThreads), 0, s, part, parts, R, C, (C + 3) & ~3, e);
     return launch_check("dense product: sum of its parts");
 }
-template moe_status dense_finish<EpiLinear>(const DensePlan &, const EpiLinear &, const float *, int, int, hipStream_t);
-template moe_status dense_finish<EpiGate>(const DensePlan &, const EpiGate &, const float *, int, int, hipStream_t);
-template moe_status dense_finish<EpiLinearBwd>(const DensePlan &, const EpiLinearBwd &, const float *, int, int, hipStream_t);
-template moe_status dense_finish<EpiGateBwd>(const DensePlan &, const EpiGateBwd &, const float *, int, int, hipStream_t);
-template moe_status dense_finish<EpiStore>(const DensePlan &, const EpiStore &, const float *, int, int, hipStream_t);
+template moe_status dense_finish<EpiLinear>(int, const EpiLinear &, const float *, int, int, hipStream_t);
+template moe_status dense_finish<EpiGate>(int, const EpiGate &, const float *, int, int, hipStream_t);
+template moe_status dense_finish<EpiLinearBwd>(int, const EpiLinearBwd &, const float *, int, int, hipStream_t);
+template moe_status dense_finish<EpiGateBwd>(int, const EpiGateBwd &, const float *, int, int, hipStream_t);
+template moe_status dense_finish<EpiStore>(int, const EpiStore &, const float *, int, int, hipStream_t);
 
 moe_status dense_gate_bwd_saved(const EpiGateBwd &e, const uint16_t *pre, int R, hipStream_t s) {
     hipLaunchKernelGGL(gate_bwd_saved_kernel, block_grid(R, kFinishRows, e.C), dim3(kThreads), 0, s, pre, R, e);

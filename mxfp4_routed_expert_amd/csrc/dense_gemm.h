@@ -317,14 +317,15 @@ moe_status dense_launch(const DenseProduct &p, const DensePlan &pl, const Epi &e
 // The product with its epilogue: in one kernel, or as parts summed by a second one.
 template <int FORM, class Epi>
 moe_status dense_run(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s) {
-    if (pl.split == 1) return dense_launch<FORM>(p, pl, e, s);
+    if (pl.split * p.terms == 1) return dense_launch<FORM>(p, pl, e, s);
     const int ld = (p.C + 3) & ~3;
     EpiPartial<Epi::kPair> ep;
     ep.part = part;
     ep.plane = (size_t)p.R * ld;
     ep.ld = ld;
     MOE_TRY((dense_launch<FORM>(p, pl, ep, s)));
-    return dense_finish(pl, e, part, p.R, p.C, s);
+    // a part's terms lie one after the other, like further parts
+    return dense_finish(pl.split * p.terms, e, part, p.R / p.terms, p.C, s);
 }
 
 }  // namespace moe

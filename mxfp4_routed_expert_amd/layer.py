@@ -219,6 +219,10 @@ class MoELayer:
         return self.out
 
 
+# Token counts up to which DenseFFN keeps h in float32 (where the library keeps low terms too)
+FFN_F32_TOKENS = 64
+
+
 class DenseFFN:
     """A dense gated feed-forward block (bf16 weights): y = (act_fn(x Wg^T) * (x Wu^T)) Wd^T + residual, and its
     training step.
@@ -240,13 +244,16 @@ class DenseFFN:
             raise ValueError(f"an MXFP8 checkpoint needs d_model a multiple of 32 (got {d})")
         bf, u8 = torch.bfloat16, torch.uint8
         e = lambda *s, dt=bf: torch.empty(s, dtype=dt, device=dev)
-        self.h, self.y = e(T, f), e(T, d)
+        # h between the products: float32 while the weights' bytes bound them (it costs nothing), else bf16;
+        # its gradient float32 always (read once by an epilogue)
+        ht = torch.float32 if T <= FFN_F32_TOKENS else bf
+        self.h, self.y = e(T, f, dt=ht), e(T, d)
         self.x_saved = (e(T, d, dt=u8), e(T, d // 32, dt=u8)) if mx else None
         self.saved = None                      # (x or codes, scales or None) of the last training forward
-        self.dh, self.dx = e(T, f), e(T, d)
+        self.dh, self.dx = e(T, f, dt=torch.float32), e(T, d)
         self.dwg, self.dwu, self.dwd = e(f, d), e(f, d), e(d, f)
-        need = max(B.moe_dense_gateup_workspace(T, d, f, act_fn), B.moe_dense_linear_workspace(T, d, f),
-                   B.moe_dense_linear_backward_workspace(T, d, f),
+        need = max(B.moe_dense_gateup_workspace(T, d, f, act_fn, ht), B.moe_dense_linear_workspace(T, d, f, x_dtype=ht),
+                   B.moe_dense_linear_backward_workspace(T, d, f, x_dtype=ht),
                    B.moe_dense_gateup_backward_workspace(T, d, f, act_fn, mx))
         self.ws = B._workspace(need, dev)
 

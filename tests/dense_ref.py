@@ -7,7 +7,8 @@ Bounds, per element, from the rounding steps of the kernels (bf16 products are e
   within 32 float32 roundings of (1 + |z|);
   a value rounded to bf16 is within 2^-8 of itself (2^-133 below the normal range);
   relu's derivative is either value where z lies within its own error of 0.
-The intermediate dz (dg, du) is rounded to bf16 before the gradient products and nowhere else.
+The intermediate dz (dg, du) is rounded to bf16 before the gradient products, when there are more than 64
+tokens, and nowhere else; up to there two bf16 terms stand for it, within 2^-16.
 """
 from __future__ import annotations
 
@@ -88,31 +89,39 @@ def gated(g, eg, u, eu, fn, dtype):
     return h, rounded(h, ea * (u.abs() + eu) + a.abs() * eu + 2 * EPS32 * h.abs(), dtype)
 
 
-def grads(dz, edz, x, w):
-    """From dz (exact) and the bound of its unrounded float32 value: dx, dw, dbias with their bounds."""
+def grads(dz, edz, x, w, dx_dtype=torch.bfloat16, exact_dz=False):
+    """From dz (exact) and the bound of its unrounded float32 value: dx, dw, dbias with their bounds.  exact_dz: dz is
+    bf16 as it stands.  A float32 x enters dw as two bf16 terms, within 2^-15 (two truncations)."""
+    xs = 2.0 ** -15 if x.dtype == torch.float32 else 0.0
     x, w = x.double(), w.double()
     n, k, T = w.shape[0], w.shape[1], x.shape[0]
-    er = rounded(dz, edz, torch.bfloat16)
+    if exact_dz:
+        er = edz
+    elif T <= 64:
+        er = edz + 2.0 ** -16 * (dz.abs() + edz) + TINY
+    else:
+        er = rounded(dz, edz, torch.bfloat16)
     m = dz.abs() + er
     dx, dw, db = dz @ w, dz.t() @ x, dz.sum(0)
     ex = er @ w.abs() + (n + 8) * EPS32 * (m @ w.abs())
-    ew = er.t() @ x.abs() + (T + 8) * EPS32 * (m.t() @ x.abs())
+    # (dz's low term, within 2^-8 of it, meets x's first term alone: 2^-8 times x's truncation of 2^-7 more)
+    ew = er.t() @ x.abs() + ((3 * T + 8) * EPS32 + xs * 2) * (m.t() @ x.abs())
     eb = edz.sum(0) + (T + 8) * EPS32 * (dz.abs() + edz).sum(0) + TINY
-    return (dx, rounded(dx, ex, torch.bfloat16)), (dw, rounded(dw, ew, torch.bfloat16)), (db, eb)
+    return (dx, rounded(dx, ex, dx_dtype)), (dw, rounded(dw, ew, torch.bfloat16)), (db, eb)
 
 
-def linear_backward(dy, x, w, bias, fn):
+def linear_backward(dy, x, w, bias, fn, dx_dtype=torch.bfloat16):
     dy = dy.double()
     if fn == "none":
-        return grads(dy, torch.zeros_like(dy), x, w)
+        return grads(dy, torch.zeros_like(dy), x, w, dx_dtype, exact_dz=True)
     z, ez = product(x, w, bias)
     d = act(fn, z)[1]
     ed = act_bound(fn, z, ez)[1]
     dz = dy * d
-    return grads(dz, dy.abs() * ed + 2 * EPS32 * dz.abs(), x, w)
+    return grads(dz, dy.abs() * ed + 2 * EPS32 * dz.abs(), x, w, dx_dtype)
 
 
-def gateup_backward(dh, x, wg, wu, bg, bu, fn, pre=None):
+def gateup_backward(dh, x, wg, wu, bg, bu, fn, pre=None, h_dtype=torch.bfloat16):
     """((dx, dw_gate, dw_up, db_gate, db_up, h), each with its bound)"""
     dh = dh.double()
     if pre is None:
@@ -129,7 +138,7 @@ def gateup_backward(dh, x, wg, wu, bg, bu, fn, pre=None):
     (xg, exg), (wgd, ewg), (bgd, ebg) = grads(dg, edg, x, wg)
     (xu, exu), (wud, ewu), (bud, ebu) = grads(du, edu, x, wu)
     return (xg + xu, exg + exu + BF16 * (xg + xu).abs()), (wgd, ewg), (wud, ewu), (bgd, ebg), (bud, ebu), \
-        gated(g, eg, u, eu, fn, torch.bfloat16)
+        gated(g, eg, u, eu, fn, h_dtype)
 
 
 def check(got, ref, what):

@@ -65,7 +65,8 @@ def test_linear_backward_refusals():
         return lib.moe_dense_linear_backward(d, dy, x, xs, w, b, dx, dw, db, ws, n, None)
     bad = B.MOE_ERR_INVALID_ARG
     refused(call(dx=None, dw=None, db=None), bad, "no gradient")
-    refused(call(d=lin(x_dtype=1)), bad, "x_dtype 1")
+    refused(call(d=lin(x_dtype=3)), bad, "x_dtype 3")
+    refused(call(d=lin(dx_dtype=2)), bad, "dx_dtype 2")
     refused(call(d=lin(x_dtype=2, kdim=40), xs=P), bad, "kdim = 40")
     refused(call(d=lin(x_dtype=2)), bad, "x_scales")
     refused(call(dy=None), bad, "NULL")
@@ -97,6 +98,7 @@ def test_gateup_refusals():
     def call(dh=P, x=P, xs=None, wg=P, wu=P, pre=None, dx=P, dwg=P, dwu=P, dbg=P, dbu=P, h=P, ws=P, n=BIG, d=gate()):
         return lib.moe_dense_gateup_backward(d, dh, x, xs, wg, wu, None, None, pre, dx, dwg, dwu, dbg, dbu, h, ws, n, None)
     bad = B.MOE_ERR_INVALID_ARG
+    refused(call(d=gate(dh_dtype=2)), bad, "dh_dtype 2")
     refused(call(dwg=None), bad, "together")
     refused(call(dbu=None), bad, "together")
     refused(call(dx=None, dwg=None, dwu=None, dbg=None, dbu=None, h=None), bad, "no result")

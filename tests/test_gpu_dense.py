@@ -147,6 +147,17 @@ def test_linear_backward(M, T, n, k, fn):
         assert torch.equal(one[j], got[j]) and all(o is None for o in one[:j] + one[j + 1:])
 
 
+@pytest.mark.parametrize("T,n,k", [(1, 40, 64), (9, 33, 72), (64, 136, 264), (65, 100, 136), (300, 264, 200)])
+@pytest.mark.parametrize("fn", ["none", "silu"])
+def test_linear_backward_float32(M, T, n, k, fn):
+    x, w, b, _ = lin_inputs(T, n, k, True, False, xt=f32, seed=T)
+    dy = rnd(T + 9, T, n)
+    got = M.moe_dense_linear_backward(dy, x, w, b, fn, dx_dtype=f32)
+    assert got[0].dtype == f32 and got[1].dtype == bf16
+    for name, g, r in zip(("dx", "dw", "dbias"), got, R.linear_backward(dy, x, w, b, fn, f32)):
+        R.check(g, r, name)
+
+
 @pytest.mark.parametrize("fn", FNS)
 def test_linear_backward_activations(M, fn):
     x, w, b, _ = lin_inputs(50, 96, 128, True, False, seed=7)
@@ -181,6 +192,18 @@ def test_gateup_backward(M, T, d, f, saved):
     if saved:      # neither the products' input nor its weight gradient is needed for dx
         part = M.moe_dense_gateup_backward(dh, None, wg, wu, bg, bu, fn, pre=pre, want=("dx",))
         assert torch.equal(part[0], got[0])
+
+
+@pytest.mark.parametrize("T", [1, 40, 64, 65, 200])
+def test_gateup_backward_float32_dh(M, T):
+    d, f = 136, 264
+    x, wg, wu, dh = rnd(1, T, d), rnd(2, f, d, std=d ** -0.5), rnd(3, f, d, std=d ** -0.5), rnd(5, T, f, dtype=f32)
+    for pre in (None, M.moe_dense_gateup(x, wg, wu, want_pre=True)[1]):
+        got = M.moe_dense_gateup_backward(dh, x, wg, wu, pre=pre, want_h=True, h_dtype=f32)
+        assert got[5].dtype == f32
+        ref = R.gateup_backward(dh, x, wg, wu, None, None, "silu", pre, f32)
+        for name, g, r in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up", "h"), got, ref):
+            R.check(g, r, name)
 
 
 @pytest.mark.parametrize("rows,cols,dt", [(1, 32, bf16), (3, 64, f32), (77, 96, bf16), (130, 416, f32), (64, 7168, bf16)])
@@ -266,14 +289,20 @@ def test_no_tokens(M):
 
 
 def _block_ref(x, xb, wg, wu, wd, res, dy):
-    """float64 block and gradients with the block's own roundings of h and dh to bf16 counted in the bound."""
-    h, eh = R.gateup(x, wg, wu, None, None, "silu", bf16)
+    """float64 block and gradients; h is rounded to bf16 between the products beyond 64 tokens, its gradient never."""
+    T = x.shape[0]
+    few = T <= 64
+    ht = f32 if few else bf16
+    g, eg = R.product(x, wg)
+    u, eu = R.product(x, wu)
+    h, eh = R.gated(g, eg, u, eu, "silu", ht)
+    wa = wd.double().abs()
     y = h @ wd.double().t() + res.double()
-    ey = eh @ wd.double().abs().t() + (h.shape[1] + 8) * R.EPS32 * (h.abs() + eh) @ wd.double().abs().t()
-    dh, edh = dy.double() @ wd.double(), None
-    edh = R.rounded(dh, (dy.shape[1] + 8) * R.EPS32 * (dy.double().abs() @ wd.double().abs()), bf16)
-    (dx, ex), (dwg, ewg), (dwu, ewu), _, _, (h2, eh2) = R.gateup_backward(dh, xb, wg, wu, None, None, "silu")
-    # dh's own rounding passes through the gradients linearly
+    ey = eh @ wa.t() + (h.shape[1] + 8) * R.EPS32 * (h.abs() + eh) @ wa.t()
+    dh, edh = R.product(dy, wd.t())
+    out = R.gateup_backward(dh, xb, wg, wu, None, None, "silu", h_dtype=ht)
+    (dx, ex), (dwg, ewg), (dwu, ewu), _, _, (h2, eh2) = out
+    # dh's own error passes through the gradients linearly (their bounds leave 2% for its square)
     g, _ = R.product(xb, wg)
     u, _ = R.product(xb, wu)
     a, d = R.act("silu", g)
@@ -281,9 +310,10 @@ def _block_ref(x, xb, wg, wu, wd, res, dy):
     ex = ex + pg @ wg.double().abs() + pu @ wu.double().abs()
     ewg = ewg + pg.t() @ xb.double().abs()
     ewu = ewu + pu.t() @ xb.double().abs()
+    da = dy.double().abs().t()
     dwd = dy.double().t() @ h2
-    ewd = R.rounded(dwd, dy.double().abs().t() @ eh2 + (x.shape[0] + 8) * R.EPS32 * (dy.double().abs().t() @ (h2.abs() + eh2)), bf16)
-    return (y, R.rounded(y, ey, bf16)), (dx, ex), (dwg, ewg), (dwu, ewu), (dwd, ewd)
+    ewd = da @ eh2 + ((2 * T + 8) * R.EPS32 + (2.0 ** -14 if few else 0.0)) * (da @ (h2.abs() + eh2))
+    return (y, R.rounded(y, ey, bf16)), (dx, ex), (dwg, ewg), (dwu, ewu), (dwd, R.rounded(dwd, ewd, bf16))
 
 
 @pytest.mark.parametrize("T,d,f", [(1, 64, 72), (24, 96, 136), (260, 288, 520)])
@@ -375,7 +405,9 @@ def test_binding_refusals(M):
          if M.binding.moe_dense_linear_workspace(64, 40, 64) > 8 else M.binding.check(3)),
         (ValueError, lambda: M.moe_dense_linear_backward(r, x, w, want=())),
         (ValueError, lambda: M.moe_dense_linear_backward(r, x, w, want=("dy",))),
-        (TypeError, lambda: M.moe_dense_linear_backward(r, x.float(), w)),
+        (TypeError, lambda: M.moe_dense_linear_backward(r, x.half(), w)),
+        (TypeError, lambda: M.moe_dense_linear_backward(r, x, w, dx_dtype=torch.half)),
+        (TypeError, lambda: M.moe_dense_gateup_backward(r, x.float(), w, w)),
         (M.MoeError, lambda: M.moe_dense_linear_backward(r, None, w, want=("dw",))),
         (ValueError, lambda: M.moe_dense_gateup(x, w, w[:8].contiguous())),
         (ValueError, lambda: M.moe_mxfp8_dequant(x.view(torch.uint8)[:, :64].contiguous(), torch.zeros(4, 3, dtype=torch.uint8, device="cuda"))),
