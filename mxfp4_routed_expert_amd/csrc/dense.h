@@ -29,89 +29,176 @@ MOE_DEV f32x4 load4_bf16(const uint16_t *p) {
 MOE_DEV uint16_t bf16_bits(float v) { return (uint16_t)(pack2_bf16(v, 0.0f) & 0xffffu); }
 
 // ------------------------------------------------------------------ activations
-// f(z) and f'(z) in float32.
+// f(z) and f'(z) in float32, on the hardware's exp2 and reciprocal (each within 1 ulp).
 //   silu       z s(z), s the logistic function          f' = s (1 + z (1 - s))
-//   gelu       z Phi(z), Phi(z) = erfc(-z / sqrt 2) / 2  f' = Phi + z exp(-z^2/2) / sqrt(2 pi)
+//   gelu       z Phi(z), Phi the normal distribution     f' = Phi + z exp(-z^2/2) / sqrt(2 pi)
 //   gelu_tanh  0.5 z (1 + tanh q) = z s(2q), q = sqrt(2/pi) (z + 0.044715 z^3): the logistic form
 //              has no cancellation for negative z         f' = s + z s (1 - s) 2q'
 //   relu       max(z, 0) (NaN stays NaN)                 f' = [z > 0]
-// 1 - s is taken as s(-t), so it keeps its relative accuracy where s rounds to 1.
+// 1 - s is taken as e s with e = exp(-t), so it keeps its relative accuracy where s rounds to 1.
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluA = 1.5957691216057308f;           // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
 MOE_DEV float gelu_arg(float z) { return z * (kGeluA + (kGeluA * kGeluB) * z * z); }
+// exp(-t), held below infinity so that its product with a zero stays zero
+MOE_DEV float exp_neg(float t) { return fminf(__builtin_amdgcn_exp2f(-kLog2e * t), 1e38f); }
+MOE_DEV float rcp(float v) { return __builtin_amdgcn_rcpf(v); }
 
-MOE_DEV float act_f(int fn, float z) {
-    if (fn == MOE_FN_NONE) return z;
-    if (fn == MOE_FN_RELU) return z < 0.0f ? 0.0f : z;
-    if (fn == MOE_FN_GELU) return 0.5f * z * erfcf(-0.70710678118654752f * z);
-    const float t = fn == MOE_FN_SILU ? z : gelu_arg(z);
-    return z / (1.0f + expf(-t));
+// erfc(x) / 2 for x = |z| / sqrt 2, given E = exp(-z^2 / 2): E times a polynomial in t = 1 / (1 + 0.4 x)
+// (least-squares fit of erfc(x) exp(x^2) / 2 with equalised relative error, 1.3e-7 over x >= 0).  Phi is that for
+// negative z and 1 minus it otherwise: no cancellation on either side.
+MOE_DEV float phi_of(float z, float E) {
+    const float t = rcp(fmaf(0.28284271f, fabsf(z), 1.0f));
+    float q = 0.025137422606348991f;
+    q = fmaf(q, t, -0.09147657454013824f);
+    q = fmaf(q, t, 0.08458571135997772f);
+    q = fmaf(q, t, -0.0028414966072887182f);
+    q = fmaf(q, t, 0.07073443382978439f);
+    q = fmaf(q, t, 0.08426576852798462f);
+    q = fmaf(q, t, 0.10392211377620697f);
+    q = fmaf(q, t, 0.11283475160598755f);
+    q = fmaf(q, t, 0.11283793300390244f);
+    q *= t * E;
+    return z < 0.0f ? q : 1.0f - q;
+}
+MOE_DEV float gauss(float z) { return __builtin_amdgcn_exp2f((-0.5f * kLog2e) * z * z); }
+
+template <int U>
+MOE_DEV void act_rows(int fn, f32x4 (&a)[U]) {
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) a[u][q] = f(a[u][q]);
+    };
+    if (fn == MOE_FN_SILU) each([](float z) { return z * rcp(1.0f + exp_neg(z)); });
+    else if (fn == MOE_FN_GELU) each([](float z) { return z * phi_of(z, gauss(z)); });
+    else if (fn == MOE_FN_GELU_TANH) each([](float z) { return z * rcp(1.0f + exp_neg(gelu_arg(z))); });
+    else if (fn == MOE_FN_RELU) each([](float z) { return z < 0.0f ? 0.0f : z; });
 }
 
-// f(z) in a, f'(z) in d
-MOE_DEV void act_fd(int fn, float z, float &a, float &d) {
-    if (fn == MOE_FN_NONE) {
-        a = z;
-        d = 1.0f;
-    } else if (fn == MOE_FN_RELU) {
-        a = z < 0.0f ? 0.0f : z;
-        d = z > 0.0f ? 1.0f : 0.0f;
+// f(z) in z's place, f'(z) in d
+template <int U>
+MOE_DEV void act_grad_rows(int fn, f32x4 (&z)[U], f32x4 (&d)[U]) {
+    auto each = [&](auto f) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v = z[u][q], g;
+                f(v, g);
+                z[u][q] = v;
+                d[u][q] = g;
+            }
+    };
+    auto logistic = [](float &v, float t, float dt, float &g) {
+        const float e = exp_neg(t), s = rcp(1.0f + e);
+        v *= s;
+        g = s + v * (e * s * dt);
+    };
+    if (fn == MOE_FN_SILU) {
+        each([&](float &v, float &g) { logistic(v, v, 1.0f, g); });
     } else if (fn == MOE_FN_GELU) {
-        const float phi = 0.5f * erfcf(-0.70710678118654752f * z);
-        a = z * phi;
-        d = phi + z * (0.39894228040143268f * expf(-0.5f * z * z));
+        each([](float &v, float &g) {
+            const float z = v, E = gauss(z), p = phi_of(z, E);
+            v = z * p;
+            g = p + z * (0.39894228040143268f * E);
+        });
+    } else if (fn == MOE_FN_GELU_TANH) {
+        each([&](float &v, float &g) { logistic(v, gelu_arg(v), kGeluA + (3.0f * kGeluA * kGeluB) * v * v, g); });
+    } else if (fn == MOE_FN_RELU) {
+        each([](float &v, float &g) {
+            g = v > 0.0f ? 1.0f : 0.0f;
+            v = v < 0.0f ? 0.0f : v;
+        });
     } else {
-        const bool si = fn == MOE_FN_SILU;
-        const float t = si ? z : gelu_arg(z);
-        const float s = 1.0f / (1.0f + expf(-t)), c = 1.0f / (1.0f + expf(t));
-        const float dt = si ? 1.0f : kGeluA + (3.0f * kGeluA * kGeluB) * z * z;
-        a = z * s;
-        d = s + a * (c * dt);
+        each([](float &, float &g) { g = 1.0f; });
     }
 }
 
 // ------------------------------------------------------------------ epilogues
-// apply(r, c, a, b, ca, cb): columns c .. c+3 of row r (c a multiple of 4); a is the product, b
-// the second matrix's when kPair.  With kColSum, ca / cb return what column sums add.  Columns
-// at or past C hold nothing and are not stored.  Rows of C columns are accessed 4 at a time when
-// C is a multiple of 4 (then every row start is aligned for it), else one at a time.
+// rows(cols(c), r, step, R, c, a, b, ca, cb): columns c .. c+3 (c a multiple of 4) of the rows r, r + step,
+// ... below R, U of them: a is the product, b the second matrix's when kPair.  The U rows' loads go out
+// together and every choice is made once for them.  With kColSum, what the rows add to the column sums
+// is added to ca / cb.  Columns at or past C hold nothing and are not stored.  Rows of C columns are
+// accessed 4 at a time when C is a multiple of 4 (then every row start is aligned for it), else one at
+// a time.
+constexpr f32x4 kZero4 = {0.f, 0.f, 0.f, 0.f};
+
+template <int U>
+MOE_DEV void load_rows(f32x4 (&v)[U], const void *p, bool f32, int C, int r, int step, int R, int c) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const size_t o = (size_t)min(r + u * step, R - 1) * C + c;
+        if (f32) v[u] = *(const f32x4 *)((const float *)p + o);
+        else v[u] = load4_bf16((const uint16_t *)p + o);
+    }
+}
+template <int U>
+MOE_DEV void store_rows(const f32x4 (&v)[U], void *p, bool f32, int ld, int r, int step, int R, int c) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (r + u * step < R) {
+            const size_t o = (size_t)(r + u * step) * ld + c;
+            if (f32) *(f32x4 *)((float *)p + o) = v[u];
+            else store4_bf16((uint16_t *)p + o, v[u]);
+        }
+}
+MOE_DEV f32x4 load_bias(const float *b, int c, int C) {
+    f32x4 v = kZero4;
+    if (b == nullptr) return v;
+    if ((C & 3) == 0) return *(const f32x4 *)(b + c);
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (c + q < C) v[q] = b[c + q];
+    return v;
+}
 
 // y = f(z + bias) + residual
 struct EpiLinear {
     static constexpr bool kPair = false, kColSum = false;
     const float *bias;
-    const void *res;      // y's type, or NULL
+    const void *res;      // y's type, or NULL; may be y
     void *y;
     int C, fn, y_f32;
     float *cs = nullptr;
-    MOE_DEV void apply(int r, int c, f32x4 a, f32x4, f32x4 &, f32x4 &) const {
-        const size_t o = (size_t)r * C + c;
-        if ((C & 3) == 0) {
-            if (bias) a += *(const f32x4 *)(bias + c);
+    int csld = 0;
+    struct Cols {
+        f32x4 bias;
+    };
+    MOE_DEV Cols cols(int c) const { return Cols{load_bias(bias, c, C)}; }
+    template <int U>
+    MOE_DEV void rows(const Cols &k, int r, int step, int R, int c, f32x4 (&a)[U], f32x4 (&)[U], f32x4 &, f32x4 &) const {
+        f32x4 add[U];
+        const bool vec = (C & 3) == 0;
+        if (res && vec) load_rows(add, res, y_f32, C, r, step, R, c);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) a[q] = act_f(fn, a[q]);
-            if (y_f32) {
-                if (res) a += *(const f32x4 *)((const float *)res + o);
-                *(f32x4 *)((float *)y + o) = a;
-            } else {
-                if (res) a += load4_bf16((const uint16_t *)res + o);
-                store4_bf16((uint16_t *)y + o, a);
+        for (int u = 0; u < U; ++u) a[u] += k.bias;
+        act_rows(fn, a);
+        if (vec) {
+            if (res) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) a[u] += add[u];
             }
-        } else {
+            store_rows(a, y, y_f32, C, r, step, R, c);
+            return;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if (c + q >= C) break;
-                float v = act_f(fn, a[q] + (bias ? bias[c + q] : 0.0f));
+                if (r + u * step >= R || c + q >= C) continue;
+                const size_t o = (size_t)(r + u * step) * C + c + q;
+                float v = a[u][q];
                 if (y_f32) {
-                    if (res) v += ((const float *)res)[o + q];
-                    ((float *)y)[o + q] = v;
+                    if (res) v += ((const float *)res)[o];
+                    ((float *)y)[o] = v;
                 } else {
-                    if (res) v += bf16_to_f32(((const uint16_t *)res)[o + q]);
-                    ((uint16_t *)y)[o + q] = bf16_bits(v);
+                    if (res) v += bf16_to_f32(((const uint16_t *)res)[o]);
+                    ((uint16_t *)y)[o] = bf16_bits(v);
                 }
             }
-        }
     }
 };
 
@@ -125,18 +212,26 @@ struct EpiGate {
     size_t plane;         // R * C
     int C, fn, h_f32;
     float *cs = nullptr;
-    MOE_DEV void apply(int r, int c, f32x4 a, f32x4 b, f32x4 &, f32x4 &) const {
-        const size_t o = (size_t)r * C + c;
-        if (bg) a += *(const f32x4 *)(bg + c);
-        if (bu) b += *(const f32x4 *)(bu + c);
-        if (pre) {
-            store4_bf16(pre + o, a);
-            store4_bf16(pre + plane + o, b);
-        }
+    int csld = 0;
+    struct Cols {
+        f32x4 bg, bu;
+    };
+    MOE_DEV Cols cols(int c) const { return Cols{load_bias(bg, c, C), load_bias(bu, c, C)}; }
+    template <int U>
+    MOE_DEV void rows(const Cols &k, int r, int step, int R, int c, f32x4 (&a)[U], f32x4 (&b)[U], f32x4 &, f32x4 &) const {
 #pragma unroll
-        for (int q = 0; q < 4; ++q) a[q] = act_f(fn, a[q]) * b[q];
-        if (h_f32) *(f32x4 *)((float *)h + o) = a;
-        else store4_bf16((uint16_t *)h + o, a);
+        for (int u = 0; u < U; ++u) {
+            a[u] += k.bg;
+            b[u] += k.bu;
+        }
+        if (pre) {
+            store_rows(a, pre, false, C, r, step, R, c);
+            store_rows(b, pre + plane, false, C, r, step, R, c);
+        }
+        act_rows(fn, a);
+#pragma unroll
+        for (int u = 0; u < U; ++u) a[u] *= b[u];
+        store_rows(a, h, h_f32, C, r, step, R, c);
     }
 };
 
@@ -159,8 +254,8 @@ MOE_DEV f32x4 low_terms(const f32x4 v) {
 }
 
 // dz = dy * f'(z + bias), rounded to bf16 for the two gradient products (and its low terms, when
-// lo is given); the bias gradient sums the unrounded values.  dz rows are ldz >= C wide (a multiple of 8); the columns past C are
-// written as zeros, so the products may read whole 16-byte chunks.
+// lo is given); the bias gradient sums the unrounded values.  dz rows are ldz >= C wide (a multiple
+// of 8); the columns past C are written as zeros, so the products may read whole 16-byte chunks.
 struct EpiLinearBwd {
     static constexpr bool kPair = false, kColSum = true;
     const float *bias;
@@ -169,33 +264,43 @@ struct EpiLinearBwd {
     int C, ldz, fn;
     float *cs;            // column-sum partials [..][csld] or NULL
     int csld;
-    MOE_DEV void apply(int r, int c, f32x4 a, f32x4, f32x4 &ca, f32x4 &) const {
-        const size_t o = (size_t)r * C + c;
-        f32x4 g = {0.f, 0.f, 0.f, 0.f};
+    struct Cols {
+        f32x4 bias;
+    };
+    MOE_DEV Cols cols(int c) const { return Cols{load_bias(bias, c, C)}; }
+    template <int U>
+    MOE_DEV void rows(const Cols &k, int r, int step, int R, int c, f32x4 (&a)[U], f32x4 (&)[U], f32x4 &ca, f32x4 &) const {
+        f32x4 g[U], d[U];
         if ((C & 3) == 0) {
-            if (bias) a += *(const f32x4 *)(bias + c);
-            g = load4_bf16(dy + o);
+            load_rows(g, dy, false, C, r, step, R, c);
         } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (c + q < C) {
-                    a[q] += bias ? bias[c + q] : 0.0f;
-                    g[q] = bf16_to_f32(dy[o + q]);
-                }
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    g[u][q] = c + q < C ? bf16_to_f32(dy[(size_t)min(r + u * step, R - 1) * C + c + q]) : 0.0f;
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float f, d;
-            act_fd(fn, a[q], f, d);
-            ca[q] = c + q < C ? g[q] * d : 0.0f;
+        for (int u = 0; u < U; ++u) a[u] += k.bias;
+        act_grad_rows(fn, a, d);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[u][q] = c + q < C ? g[u][q] * d[u][q] : 0.0f;
+            if (r + u * step < R) ca += d[u];
         }
         const bool tail = c + 4 >= C && c + 4 < ldz;
-        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
-        store4_bf16(dz + (size_t)r * ldz + c, ca);
-        if (tail) store4_bf16(dz + (size_t)r * ldz + c + 4, zero);
+        store_rows(d, dz, false, ldz, r, step, R, c);
         if (lo) {
-            store4_bf16(lo + (size_t)r * ldz + c, low_terms(ca));
-            if (tail) store4_bf16(lo + (size_t)r * ldz + c + 4, zero);
+#pragma unroll
+            for (int u = 0; u < U; ++u) d[u] = low_terms(d[u]);
+            store_rows(d, lo, false, ldz, r, step, R, c);
+        }
+        if (tail) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) d[u] = kZero4;
+            store_rows(d, dz, false, ldz, r, step, R, c + 4);
+            if (lo) store_rows(d, lo, false, ldz, r, step, R, c + 4);
         }
     }
 };
@@ -212,32 +317,45 @@ struct EpiGateBwd {
     int C, fn, dh_f32, h_f32;
     float *cs;            // column-sum partials [..][csld], csld = 2C, or NULL
     int csld;
-    MOE_DEV void apply(int r, int c, f32x4 a, f32x4 b, f32x4 &ca, f32x4 &cb) const {
-        if (bg) a += *(const f32x4 *)(bg + c);
-        if (bu) b += *(const f32x4 *)(bu + c);
-        grads(r, c, a, b, ca, cb);
-    }
-    MOE_DEV void grads(int r, int c, f32x4 g, f32x4 u, f32x4 &ca, f32x4 &cb) const {
-        const size_t o = (size_t)r * C + c;
-        const f32x4 d = dh_f32 ? *(const f32x4 *)((const float *)dh + o) : load4_bf16((const uint16_t *)dh + o);
-        f32x4 hv;
+    struct Cols {
+        f32x4 bg, bu;
+    };
+    MOE_DEV Cols cols(int c) const { return Cols{load_bias(bg, c, C), load_bias(bu, c, C)}; }
+    template <int U>
+    MOE_DEV void rows(const Cols &k, int r, int step, int R, int c, f32x4 (&a)[U], f32x4 (&b)[U], f32x4 &ca, f32x4 &cb) const {
+        f32x4 d[U], df[U];
+        load_rows(d, dh, dh_f32, C, r, step, R, c);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float f, df;
-            act_fd(fn, g[q], f, df);
-            ca[q] = d[q] * u[q] * df;
-            cb[q] = d[q] * f;
-            hv[q] = f * u[q];
+        for (int u = 0; u < U; ++u) {
+            a[u] += k.bg;
+            b[u] += k.bu;
         }
-        store4_bf16(dgu + (size_t)r * 2 * C + c, ca);
-        store4_bf16(dgu + (size_t)r * 2 * C + C + c, cb);
-        if (lo) {
-            store4_bf16(lo + (size_t)r * 2 * C + c, low_terms(ca));
-            store4_bf16(lo + (size_t)r * 2 * C + C + c, low_terms(cb));
-        }
+        act_grad_rows(fn, a, df);
         if (h) {
-            if (h_f32) *(f32x4 *)((float *)h + o) = hv;
-            else store4_bf16((uint16_t *)h + o, hv);
+            f32x4 hv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) hv[u] = a[u] * b[u];
+            store_rows(hv, h, h_f32, C, r, step, R, c);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            b[u] = d[u] * b[u] * df[u];      // dg
+            a[u] = d[u] * a[u];              // du
+            if (r + u * step < R) {
+                ca += b[u];
+                cb += a[u];
+            }
+        }
+        store_rows(b, dgu, false, 2 * C, r, step, R, c);
+        store_rows(a, dgu, false, 2 * C, r, step, R, C + c);
+        if (lo) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                b[u] = low_terms(b[u]);
+                a[u] = low_terms(a[u]);
+            }
+            store_rows(b, lo, false, 2 * C, r, step, R, c);
+            store_rows(a, lo, false, 2 * C, r, step, R, C + c);
         }
     }
 };
@@ -249,25 +367,20 @@ struct EpiStore {
     void *out0, *out1;
     int rows0, C, f32;
     float *cs = nullptr;
-    MOE_DEV void apply(int r, int c, f32x4 a, f32x4, f32x4 &, f32x4 &) const {
-        void *p = r < rows0 ? out0 : out1;
-        const size_t o = (size_t)(r < rows0 ? r : r - rows0) * C + c;
-        if (f32) *(f32x4 *)((float *)p + o) = a;
-        else store4_bf16((uint16_t *)p + o, a);
-    }
-};
-
-// float32 partial results of one part of a split sum: [split][mats][R][ld], ld = C rounded up to 4.
-template <bool PAIR>
-struct EpiPartial {
-    static constexpr bool kPair = PAIR, kColSum = false;
-    float *part;          // this part's first matrix
-    size_t plane;         // R * ld
-    int ld;
-    float *cs = nullptr;
-    MOE_DEV void apply(int r, int c, f32x4 a, f32x4 b, f32x4 &, f32x4 &) const {
-        *(f32x4 *)(part + (size_t)r * ld + c) = a;
-        if constexpr (PAIR) *(f32x4 *)(part + plane + (size_t)r * ld + c) = b;
+    int csld = 0;
+    struct Cols {};
+    MOE_DEV Cols cols(int) const { return Cols{}; }
+    template <int U>
+    MOE_DEV void rows(const Cols &, int r, int step, int R, int c, f32x4 (&a)[U], f32x4 (&)[U], f32x4 &, f32x4 &) const {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int row = r + u * step;
+            if (row >= R) continue;
+            void *p = row < rows0 ? out0 : out1;
+            const size_t o = (size_t)(row < rows0 ? row : row - rows0) * C + c;
+            if (f32) *(f32x4 *)((float *)p + o) = a[u];
+            else store4_bf16((uint16_t *)p + o, a[u]);
+        }
     }
 };
 
@@ -295,16 +408,32 @@ struct DenseProduct {
     int rcols;            // TN: readable columns of a row-operand row (>= R, a multiple of 8)
 };
 
-// How a product runs: tile shape, parts of the sum.
+// How a product runs.  The first `full` tiles (whole rounds of workgroups over the CUs, or all) run with
+// the epilogue in the product kernel; the sum of each of the rest is split into `split` parts over
+// workgroups of the same launch, whose float32 results a second kernel adds up, in order, and finishes.
 struct DensePlan {
     int cfg;              // 0: 256 x 256, 1: 128 x 128, 2: 64 x 128 tiles
-    int split;            // parts of the sum (1: the epilogue runs in the product kernel)
     int tr, tc;           // tiles along rows and columns
+    int full, split;
     int steps;            // 64-value steps of the sum, all segments
     int cs_rows;          // column-sum partial rows the launch writes
+    size_t part_bytes;    // partial results
 };
 DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg, int terms = 1);
-size_t dense_plan_bytes(const DensePlan &pl, bool pair, int R, int C, int terms = 1);   // partial results
+
+// Order of the tiles: kTileGroup row tiles share each column tile, so the tiles that run together on an XCD
+// form a block and share both operands in its L2.
+constexpr int kTileGroup = 4;
+__host__ __device__ inline void tile_at(int slot, int tr, int tc, int &r, int &c) {
+    const int per = kTileGroup * tc, g = slot / per, i = slot - g * per;
+    const int n = tr - g * kTileGroup < kTileGroup ? tr - g * kTileGroup : kTileGroup;
+    r = g * kTileGroup + i % n;
+    c = i / n;
+}
+__host__ __device__ inline int tile_slot(int r, int c, int tr, int tc) {
+    const int g = r / kTileGroup, n = tr - g * kTileGroup < kTileGroup ? tr - g * kTileGroup : kTileGroup;
+    return g * kTileGroup * tc + c * n + (r - g * kTileGroup);
+}
 
 moe_status dense_linear_product(const DenseProduct &p, const DensePlan &pl, const EpiLinear &e, float *part, hipStream_t s);
 moe_status dense_gate_product(const DenseProduct &p, const DensePlan &pl, const EpiGate &e, float *part, hipStream_t s);
@@ -315,10 +444,13 @@ moe_status dense_gate_bwd_product(const DenseProduct &p, const DensePlan &pl, co
 moe_status dense_nn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, hipStream_t s);
 moe_status dense_tn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, hipStream_t s);
 
-// Sum the parts of a split product and run the epilogue on the sums (dense_aux.hip).
+// Sum the parts of the split tiles and run the epilogue on the sums (dense_aux.hip).  br x bc: the tile.
+// Partial results: [split tile][part][br][bc], a pair tile's columns gate first.
 template <class Epi>
-moe_status dense_finish(int parts, const Epi &e, const float *part, int R, int C, hipStream_t s);
-constexpr int kFinishRows = 2;    // rows per workgroup of the finish and saved-activation kernels
+moe_status dense_finish(const DenseProduct &p, const DensePlan &pl, int br, int bc, const Epi &e, const float *part,
+                        hipStream_t s);
+constexpr int kFinishRows = 16;   // rows per workgroup there, and per column-sum row of the launch
+constexpr int kSavedRows = 2;     // rows per workgroup of the saved pre-activations' gradients
 
 // out[c] = sum over rows of part[row][c] (column-sum partials), in row order.
 moe_status dense_colsum_reduce(const float *part, int rows, int ld, int C0, float *out0, float *out1, hipStream_t s);

@@ -9,15 +9,18 @@ constexpr int kCUs = 256;            // the plan is a pure function of the sizes
 
 struct Tile {
     int br, bc, wr, per_cu;
-    double step, tile;               // cost of a 64-value step of a full CU, and of a tile's start and end, in us
+    double step, tile;               // us: a 64-value step of a CU's workgroups, and a tile's start and end
 };
-constexpr Tile kTiles[3] = {{256, 256, 2, 1, 1.15, 6.0}, {128, 128, 2, 2, 0.75, 4.0}, {64, 128, 1, 3, 0.75, 3.5}};
+constexpr Tile kTiles[3] = {{256, 256, 2, 1, 1.42, 9.0}, {128, 128, 2, 2, 0.95, 5.0}, {64, 128, 1, 3, 0.95, 4.5}};
 constexpr int kMaxSplit = 16;
+constexpr double kPartBytesPerUs = 4.0e6;   // partial results written and read back
+constexpr double kFinishUs = 4.0;           // the launch that sums them
 
 }  // namespace
 
-// The tile shape and split with the least estimated time: rounds of workgroups over the CUs times
-// their steps, plus the traffic of the partial results and the launch that sums them.
+// The tile shape and split with the least estimated time.  Whole rounds of tiles over the CUs run
+// unsplit; the tiles left over either make a round of their own or are split so that their parts fill
+// one, at the cost of the partial results' traffic and a second launch.
 DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg, int terms) {
     DensePlan best = {};
     double best_t = 1e30;
@@ -25,31 +28,32 @@ DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg, int ter
     const int mats = pair ? 2 : 1;
     for (int cfg = 0; cfg < (form == kFormTN ? 2 : 3); ++cfg) {
         const Tile &t = kTiles[cfg];
-        const int tr = (R + t.br - 1) / t.br, tc = (C * mats + t.bc - 1) / t.bc;
-        const int64_t tiles = (int64_t)tr * tc;
+        const int tr = (R + t.br - 1) / t.br, tc = (C + t.bc / mats - 1) / (t.bc / mats);
+        const int64_t tiles = (int64_t)tr * tc, slots = (int64_t)kCUs * t.per_cu;
+        // rounds of n workgroups of s steps each; a last round with fewer workgroups per CU runs faster
+        auto rounds = [&](int64_t n, int s) {
+            if (n <= 0) return 0.0;
+            const int64_t k = (n + slots - 1) / slots, last = (n - (k - 1) * slots + kCUs - 1) / kCUs;
+            return ((double)(k - 1) + 0.35 + 0.65 * (double)last / t.per_cu) * (s * t.step + t.tile);
+        };
         for (int split = 1; split <= kMaxSplit; ++split) {
-            if (split > 1 && (split * 4 > steps || R > 65536 || tiles * split > 4 * kCUs)) break;
-            const int64_t wgs = tiles * split;
-            const int64_t slots = (int64_t)kCUs * t.per_cu;
-            const int64_t rounds = (wgs + slots - 1) / slots;
-            // a last round that fills fewer workgroups per CU runs its steps faster
-            const int64_t last = (wgs - (rounds - 1) * slots + kCUs - 1) / kCUs;
-            const double load = (double)(rounds - 1) + (0.35 + 0.65 * (double)last / t.per_cu);
-            double us = load * (((steps + split - 1) / split) * t.step + t.tile);
-            if (split * terms > 1) us += 3.0 + (double)R * C * mats * 4.0 * split * 2.0 / 4.0e6;
+            if (split > 1 && split * 4 > steps) break;
+            const int64_t full = split * terms == 1 ? tiles : (terms > 1 ? 0 : tiles / slots * slots), tail = tiles - full;
+            if (split > 1 && (tail == 0 || tail * split > slots)) break;
+            double us = rounds(full, steps) + rounds(tail * split, (steps + split - 1) / split);
+            const size_t bytes = (size_t)tail * split * t.br * t.bc * sizeof(float);
+            if (tail > 0) {
+                const double live = (double)(R < t.br ? R : t.br) / t.br;
+                us += kFinishUs + bytes * live * 2.0 / kPartBytesPerUs;
+            }
             if (us < best_t) {
                 best_t = us;
-                best = DensePlan{cfg, split, tr, tc, steps,
-                                 split * terms > 1 ? (R / terms + kFinishRows - 1) / kFinishRows : tr * t.wr};
+                best = DensePlan{cfg, tr, tc, (int)full, split, steps,
+                                 tail > 0 ? (R / terms + t.br - 1) / t.br * (t.br / kFinishRows) : tr * t.wr, bytes};
             }
         }
     }
     return best;
-}
-
-size_t dense_plan_bytes(const DensePlan &pl, bool pair, int R, int C, int terms) {
-    if (pl.split * terms == 1) return 0;
-    return (size_t)pl.split * (pair ? 2 : 1) * R * ((C + 3) & ~3) * sizeof(float);
 }
 
 namespace {
@@ -119,7 +123,7 @@ LinearWs linear_ws(const moe_linear_desc *d, void *base) {
     w.nseg = f32 && w.terms == 1 ? 3 : 1;
     w.plan = dense_plan(kFormNT, false, d->T * w.terms, d->n, d->kdim, w.nseg, w.terms);
     w.planes = c.take<uint16_t>(f32 ? (size_t)3 * d->T * d->kdim * 2 : 0);
-    w.part = c.take<float>(dense_plan_bytes(w.plan, false, d->T * w.terms, d->n, w.terms));
+    w.part = c.take<float>(w.plan.part_bytes);
     w.bytes = c.at;
     return w;
 }
@@ -156,8 +160,8 @@ LinearBwdWs linear_bwd_ws(const moe_linear_desc *d, void *base) {
     w.x = c.take<uint16_t>(f32 ? (size_t)3 * T * k * 2 : (d->x_dtype == MOE_DT_MXFP8 ? (size_t)T * k * 2 : 0));
     w.dz = c.take<uint16_t>(w.own_dz ? (size_t)w.dterms * T * w.ldz * 2 : 0);
     w.cs = c.take<float>((size_t)w.cs_rows * w.csld * 4);
-    size_t part = act ? dense_plan_bytes(w.pz, false, T * w.zterms, n, w.zterms) : 0;
-    const size_t bx = dense_plan_bytes(w.px, false, T * w.dterms, k, w.dterms), bw = dense_plan_bytes(w.pw, false, n, k);
+    size_t part = act ? w.pz.part_bytes : 0;
+    const size_t bx = w.px.part_bytes, bw = w.pw.part_bytes;
     part = part > bx ? part : bx;
     part = part > bw ? part : bw;
     w.part = c.take<float>(part);
@@ -199,7 +203,7 @@ GateWs gate_ws(const moe_gateup_desc *d, void *base) {
     if (d->T <= kGemvTokens) return w;
     Carve c{(char *)base};
     w.plan = dense_plan(kFormNT, true, d->T, d->d_ff, d->d_model, 1);
-    w.part = c.take<float>(dense_plan_bytes(w.plan, true, d->T, d->d_ff));
+    w.part = c.take<float>(w.plan.part_bytes);
     w.bytes = c.at;
     return w;
 }
@@ -223,12 +227,12 @@ GateBwdWs gate_bwd_ws(const moe_gateup_desc *d, void *base) {
     w.px = dense_plan(kFormNN, false, xr, d->d_model, f, 2, w.terms);
     w.pw = dense_plan(kFormTN, false, 2 * f, d->d_model, d->T, w.terms);
     w.cs_rows = w.pg.cs_rows;
-    w.cs_rows_saved = (d->T + kFinishRows - 1) / kFinishRows;
+    w.cs_rows_saved = (d->T + kSavedRows - 1) / kSavedRows;
     w.x = c.take<uint16_t>(d->x_dtype == MOE_DT_MXFP8 ? (size_t)d->T * d->d_model * 2 : 0);
     w.dgu = c.take<uint16_t>((size_t)xr * 2 * f * 2);
     w.cs = c.take<float>((size_t)(w.cs_rows > w.cs_rows_saved ? w.cs_rows : w.cs_rows_saved) * 2 * f * 4);
-    size_t part = dense_plan_bytes(w.pg, true, d->T, f);
-    const size_t bx = dense_plan_bytes(w.px, false, xr, d->d_model, w.terms), bw = dense_plan_bytes(w.pw, false, 2 * f, d->d_model);
+    size_t part = w.pg.part_bytes;
+    const size_t bx = w.px.part_bytes, bw = w.pw.part_bytes;
     part = part > bx ? part : bx;
     part = part > bw ? part : bw;
     w.part = c.take<float>(part);

@@ -20,43 +20,67 @@ MOE_DEV Block block_of(int C) {
 }
 dim3 block_grid(int R, int rows, int C) { return dim3((unsigned)((R + rows - 1) / rows) * (unsigned)col_blocks(C)); }
 
-// Column-sum partials of this thread's four (pair: eight) columns: one row per workgroup row.
-template <class Epi>
-MOE_DEV void store_colsums(const Epi &epi, int rb, int C, int c, f32x4 sa, f32x4 sb) {
+// Sum the parts of the split tiles in order (the same order on every run), the terms of a row after each
+// other, and run the epilogue.  A workgroup takes kFinishRows rows of a tile; LANES threads a row, four
+// columns each, and a thread U rows, whose loads of all parts are independent.
+template <int LANES, class Epi>
+__global__ __launch_bounds__(kThreads) void dense_finish_kernel(const float *__restrict__ part, int full, int split, int terms,
+                                                                int tr_n, int tc_n, int rows, int C, int br, Epi epi) {
+    constexpr int kStep = kThreads / LANES, U = kFinishRows / kStep;
+    constexpr int BC = LANES * 4 * (Epi::kPair ? 2 : 1);
+    static_assert(U >= 1 && U * kStep == kFinishRows, "whole rows");
+    const int blocks = br / kFinishRows;
+    const int t = blockIdx.x / blocks, rb = blockIdx.x - t * blocks;
+    int tr, tc;
+    if (terms == 1) {
+        tile_at(full + t, tr_n, tc_n, tr, tc);
+    } else {                                      // (every tile is split) output rows are the first term's
+        tr = t / tc_n;
+        tc = t - tr * tc_n;
+    }
+    const int lane = threadIdx.x % LANES, er = threadIdx.x / LANES;
+    const int c = tc * (LANES * 4) + 4 * lane, r = tr * br + rb * kFinishRows + er;
+    const bool live = c < C && r < rows;
+    f32x4 sa = kZero4, sb = kZero4;
+    if (live) {
+        f32x4 a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) a[u] = b[u] = kZero4;
+        for (int j = 0; j < terms; ++j) {
+            const float *src[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int rr = min(r + u * kStep, rows - 1) + j * rows, rt = rr / br;
+                src[u] = part + ((size_t)(tile_slot(rt, tc, tr_n, tc_n) - full) * split * br + (rr - rt * br)) * BC + 4 * lane;
+            }
+            for (int s = 0; s < split; ++s)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float *q = src[u] + (size_t)s * br * BC;
+                    a[u] += *(const f32x4 *)q;
+                    if constexpr (Epi::kPair) b[u] += *(const f32x4 *)(q + BC / 2);
+                }
+        }
+        epi.rows(epi.cols(c), r, kStep, rows, c, a, b, sa, sb);
+    }
     if constexpr (Epi::kColSum) {
         if (epi.cs) {
-            float *row = epi.cs + (size_t)rb * epi.csld;
-            *(f32x4 *)(row + c) = sa;
-            if constexpr (Epi::kPair) *(f32x4 *)(row + C + c) = sb;
+            // column sums of the workgroup's rows, one partial row
+            __shared__ f32x4 s_sum[Epi::kPair ? 2 : 1][kStep][LANES];
+            s_sum[0][er][lane] = sa;
+            if constexpr (Epi::kPair) s_sum[1][er][lane] = sb;
+            __syncthreads();
+            if (er == 0 && c < C) {
+                for (int i = 1; i < kStep; ++i) {
+                    sa += s_sum[0][i][lane];
+                    if constexpr (Epi::kPair) sb += s_sum[1][i][lane];
+                }
+                float *row = epi.cs + (size_t)(tr * blocks + rb) * epi.csld;
+                *(f32x4 *)(row + c) = sa;
+                if constexpr (Epi::kPair) *(f32x4 *)(row + C + c) = sb;
+            }
         }
     }
-}
-
-// Sum the parts in order (the same order on every run) and run the epilogue.
-template <class Epi>
-__global__ __launch_bounds__(kThreads) void dense_finish_kernel(const float *__restrict__ part, int split, int R, int C,
-                                                                int ld, Epi epi) {
-    const Block bl = block_of(C);
-    const int c = bl.cb * kCols + threadIdx.x * 4;
-    if (c >= C) return;
-    const size_t plane = (size_t)R * ld;
-    constexpr int M = Epi::kPair ? 2 : 1;
-    f32x4 sa = {0.f, 0.f, 0.f, 0.f}, sb = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kFinishRows; ++i) {
-        const int r = bl.rb * kFinishRows + i;
-        if (r >= R) break;
-        f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        const float *src = part + (size_t)r * ld + c;
-        for (int s = 0; s < split; ++s)
-#pragma unroll
-            for (int m = 0; m < M; ++m) v[m] += *(const f32x4 *)(src + (size_t)(s * M + m) * plane);
-        f32x4 ca = {0.f, 0.f, 0.f, 0.f}, cb = {0.f, 0.f, 0.f, 0.f};
-        epi.apply(r, c, v[0], v[1], ca, cb);
-        sa += ca;
-        sb += cb;
-    }
-    store_colsums(epi, bl.rb, C, c, sa, sb);
 }
 
 // Gradients of the gated product from the saved bf16 pre-activations [2][R][C].
@@ -64,18 +88,16 @@ __global__ __launch_bounds__(kThreads) void gate_bwd_saved_kernel(const uint16_t
     const Block bl = block_of(epi.C);
     const int c = bl.cb * kCols + threadIdx.x * 4;
     if (c >= epi.C) return;
-    f32x4 sa = {0.f, 0.f, 0.f, 0.f}, sb = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kFinishRows; ++i) {
-        const int r = bl.rb * kFinishRows + i;
-        if (r >= R) break;
-        const size_t o = (size_t)r * epi.C + c;
-        f32x4 ca, cb;
-        epi.grads(r, c, load4_bf16(pre + o), load4_bf16(pre + (size_t)R * epi.C + o), ca, cb);
-        sa += ca;
-        sb += cb;
+    const int r = bl.rb * kSavedRows;
+    f32x4 g[kSavedRows], u[kSavedRows], sa = kZero4, sb = kZero4;
+    load_rows(g, pre, false, epi.C, r, 1, R, c);
+    load_rows(u, pre + (size_t)R * epi.C, false, epi.C, r, 1, R, c);
+    epi.rows(EpiGateBwd::Cols{kZero4, kZero4}, r, 1, R, c, g, u, sa, sb);
+    if (epi.cs) {
+        float *row = epi.cs + (size_t)bl.rb * epi.csld;
+        *(f32x4 *)(row + c) = sa;
+        *(f32x4 *)(row + epi.C + c) = sb;
     }
-    store_colsums(epi, bl.rb, epi.C, c, sa, sb);
 }
 
 // Column sums of kColRows rows of a bf16 matrix.
@@ -167,18 +189,34 @@ __global__ __launch_bounds__(kThreads) void pad_rows_kernel(const uint16_t *__re
 }  // namespace
 
 template <class Epi>
-moe_status dense_finish(int parts, const Epi &e, const float *part, int R, int C, hipStream_t s) {
-    hipLaunchKernelGGL(dense_finish_kernel<Epi>, block_grid(R, kFinishRows, C), dim3(kThreads), 0, s, part, parts, R, C, (C + 3) & ~3, e);
+moe_status dense_finish(const DenseProduct &p, const DensePlan &pl, int br, int bc, const Epi &e, const float *part,
+                        hipStream_t s) {
+    const int rows = p.R / p.terms, blocks = br / kFinishRows;
+    const int tiles = p.terms == 1 ? pl.tr * pl.tc - pl.full : (rows + br - 1) / br * pl.tc;
+    const dim3 grid((unsigned)(tiles * blocks));
+    const int lanes = bc / 4 / (Epi::kPair ? 2 : 1);
+#define MOE_FINISH(L)                                                                                                    \
+    hipLaunchKernelGGL((dense_finish_kernel<L, Epi>), grid, dim3(kThreads), 0, s, part, pl.full, pl.split, p.terms, pl.tr, \
+                       pl.tc, rows, p.C, br, e)
+    if (lanes == 64) MOE_FINISH(64);
+    else if (lanes == 32) MOE_FINISH(32);
+    else MOE_FINISH(16);
+#undef MOE_FINISH
     return launch_check("dense product: sum of its parts");
 }
-template moe_status dense_finish<EpiLinear>(int, const EpiLinear &, const float *, int, int, hipStream_t);
-template moe_status dense_finish<EpiGate>(int, const EpiGate &, const float *, int, int, hipStream_t);
-template moe_status dense_finish<EpiLinearBwd>(int, const EpiLinearBwd &, const float *, int, int, hipStream_t);
-template moe_status dense_finish<EpiGateBwd>(int, const EpiGateBwd &, const float *, int, int, hipStream_t);
-template moe_status dense_finish<EpiStore>(int, const EpiStore &, const float *, int, int, hipStream_t);
+template moe_status dense_finish<EpiLinear>(const DenseProduct &, const DensePlan &, int, int, const EpiLinear &, const float *,
+                                            hipStream_t);
+template moe_status dense_finish<EpiGate>(const DenseProduct &, const DensePlan &, int, int, const EpiGate &, const float *,
+                                          hipStream_t);
+template moe_status dense_finish<EpiLinearBwd>(const DenseProduct &, const DensePlan &, int, int, const EpiLinearBwd &,
+                                               const float *, hipStream_t);
+template moe_status dense_finish<EpiGateBwd>(const DenseProduct &, const DensePlan &, int, int, const EpiGateBwd &,
+                                             const float *, hipStream_t);
+template moe_status dense_finish<EpiStore>(const DenseProduct &, const DensePlan &, int, int, const EpiStore &, const float *,
+                                           hipStream_t);
 
 moe_status dense_gate_bwd_saved(const EpiGateBwd &e, const uint16_t *pre, int R, hipStream_t s) {
-    hipLaunchKernelGGL(gate_bwd_saved_kernel, block_grid(R, kFinishRows, e.C), dim3(kThreads), 0, s, pre, R, e);
+    hipLaunchKernelGGL(gate_bwd_saved_kernel, block_grid(R, kSavedRows, e.C), dim3(kThreads), 0, s, pre, R, e);
     return launch_check("gated gradients");
 }
 

@@ -22,15 +22,17 @@
 
 namespace moe {
 
-struct CfgL { static constexpr int BR = 256, BC = 256, WR = 2, WC = 4; };   // 8 waves of 128 x 64
-struct CfgM { static constexpr int BR = 128, BC = 128, WR = 2, WC = 2; };   // 4 waves of 64 x 64
-struct CfgS { static constexpr int BR = 64, BC = 128, WR = 1, WC = 4; };    // 4 waves of 64 x 32
+struct CfgL { static constexpr int BR = 256, BC = 256, WR = 2, WC = 4; static constexpr bool kAlternate = true; };    // 8 waves of 128 x 64
+struct CfgM { static constexpr int BR = 128, BC = 128, WR = 2, WC = 2; static constexpr bool kAlternate = false; };   // 4 waves of 64 x 64
+struct CfgS { static constexpr int BR = 64, BC = 128, WR = 1, WC = 4; static constexpr bool kAlternate = false; };    // 4 waves of 64 x 32
 
 constexpr int kBK = 64;
 
 struct GemmArgs {
     DenseProduct p;
-    int tr, tc, split, steps, seg_steps;
+    int tr, tc, full, split, steps, seg_steps;
+    int cs_sub;           // column-sum rows per wave row of a tile
+    float *part;
 };
 
 __device__ __attribute__((aligned(16))) const uint32_t g_dense_zero[4] = {0, 0, 0, 0};
@@ -87,27 +89,26 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const
     const int wr = wave / Cfg::WC, wc = wave % Cfg::WC;
     const int lr = lane & 15, lg = lane >> 4;
 
-    // ---- which tile: XCD x (workgroups x, x + 8, ...) takes a contiguous run of the order below,
-    // in which kGroup row tiles share each column tile, so the tiles that run together on an XCD
-    // form a block and share both operands in its L2.
-    constexpr int kGroup = 4;
-    const int tiles = ga.tr * ga.tc, G = tiles * ga.split;
-    int slot;
+    // ---- which tile and part of the sum: of each launch part (full tiles, then split ones), XCD x
+    // (workgroups x, x + 8, ...) takes a contiguous run
+    const int tail = ga.tr * ga.tc - ga.full;
+    const bool split_tile = (int)blockIdx.x >= ga.full;
+    int slot, sp = 0;
     {
-        const int b = blockIdx.x, x = b & 7, q = G >> 3, rem = G & 7;
+        const int b = split_tile ? blockIdx.x - ga.full : blockIdx.x, G = split_tile ? tail * ga.split : ga.full;
+        const int x = b & 7, q = G >> 3, rem = G & 7;
         slot = x * q + min(x, rem) + (b >> 3);
+        if (split_tile) {
+            sp = slot / tail;
+            slot = ga.full + slot - sp * tail;
+        }
     }
-    const int sp = slot / tiles;
     int tr, tc;
-    {
-        const int t = slot - sp * tiles, per = kGroup * ga.tc, g = t / per, i = t - g * per;
-        const int gr = min(kGroup, ga.tr - g * kGroup);
-        tr = g * kGroup + i % gr;
-        tc = i / gr;
-    }
+    tile_at(slot, ga.tr, ga.tc, tr, tc);
     constexpr int kPairCols = BC / 2;                       // columns of each matrix in a pair tile
     const int r0 = tr * BR, c0 = tc * (PAIR ? kPairCols : BC);
-    const int s0 = (int)((int64_t)ga.steps * sp / ga.split), s1 = (int)((int64_t)ga.steps * (sp + 1) / ga.split);
+    const int parts = split_tile ? ga.split : 1;
+    const int s0 = (int)((int64_t)ga.steps * sp / parts), s1 = (int)((int64_t)ga.steps * (sp + 1) / parts);
 
     // ---- copy sources
     OpR opr;
@@ -205,54 +206,110 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const
         const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
         return __builtin_bit_cast(bf16x8, v);
     };
-    auto compute = [&](int st) {
+    bf16x8 fr[TR], fc[TC];
+    auto read = [&](int st, int ks) {
         const int base_r = st * kStage, base_c = st * kStage + OpR::kBytes;
 #pragma unroll
-        for (int ks = 0; ks < kBK / 32; ++ks) {
-            bf16x8 fr[TR], fc[TC];
+        for (int j = 0; j < TR; ++j) {
+            const int f0 = wr * 16 * TR + 16 * j;
+            if constexpr (RS) fr[j] = frag_s(base_r, f0, ks, std::integral_constant<int, BR>{});
+            else fr[j] = frag_c(base_r, f0, ks);
+        }
 #pragma unroll
-            for (int j = 0; j < TR; ++j) {
-                const int f0 = wr * 16 * TR + 16 * j;
-                if constexpr (RS) fr[j] = frag_s(base_r, f0, ks, std::integral_constant<int, BR>{});
-                else fr[j] = frag_c(base_r, f0, ks);
-            }
-#pragma unroll
-            for (int i = 0; i < TC; ++i) {
-                const int f0 = wc * 16 * TC + 16 * i;
-                if constexpr (CS) fc[i] = frag_s(base_c, f0, ks, std::integral_constant<int, BC>{});
-                else fc[i] = frag_c(base_c, f0, ks);
-            }
-#pragma unroll
-            for (int i = 0; i < TC; ++i)
-#pragma unroll
-                for (int j = 0; j < TR; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc[i], fr[j], acc[i][j], 0, 0, 0);
+        for (int i = 0; i < TC; ++i) {
+            const int f0 = wc * 16 * TC + 16 * i;
+            if constexpr (CS) fc[i] = frag_s(base_c, f0, ks, std::integral_constant<int, BC>{});
+            else fc[i] = frag_c(base_c, f0, ks);
         }
     };
+    auto multiply = [&]() {
+#pragma unroll
+        for (int i = 0; i < TC; ++i)
+#pragma unroll
+            for (int j = 0; j < TR; ++j)
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc[i], fr[j], acc[i][j], 0, 0, 0);
+    };
 
-    if (s0 < s1) issue(s0, 0);
-    for (int s = s0; s < s1; ++s) {
-        // this wave's copies of step s have landed and its reads of step s-1 are done; then all meet
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (s + 1 < s1) issue(s + 1, (s + 1 - s0) & 1);
-        compute((s - s0) & 1);
+    if constexpr (Cfg::kAlternate) {
+        // Two waves share a SIMD: wave w of the first half of the workgroup and w + NW/2 of the second.  While
+        // one multiplies (32 matrix instructions), the other reads its next operands from LDS, then they
+        // change places at a barrier: the matrix cores never wait for an LDS read.  The second half runs one
+        // phase behind.  A step is four phases of a wave: read, multiply, read, multiply.  Step s+1's copies go
+        // out in the first one (its buffer was last read, by the second half, in the phase before) and have
+        // landed when the first half reads them four phases later.
+        const bool second = wave >= NW / 2;
+        auto phase_end = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto read_end = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        auto copies_end = [&]() {
+            __builtin_amdgcn_sched_barrier(0);
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            __builtin_amdgcn_sched_barrier(0);
+        };
+        if (s0 < s1) {
+            issue(s0, 0);
+            copies_end();
+            if (second) phase_end();
+            for (int s = s0; s < s1; ++s) {
+                const int st = (s - s0) & 1;
+                if (s + 1 < s1) issue(s + 1, st ^ 1);
+                read(st, 0);
+                read_end();
+                __builtin_amdgcn_s_setprio(1);
+                multiply();
+                __builtin_amdgcn_s_setprio(0);
+                phase_end();
+                read(st, 1);
+                if (second) copies_end();
+                else read_end();
+                __builtin_amdgcn_s_setprio(1);
+                multiply();
+                __builtin_amdgcn_s_setprio(0);
+                if (second) phase_end();
+                else copies_end();
+            }
+            if (!second) phase_end();
+        }
+    } else {
+        if (s0 < s1) issue(s0, 0);
+        for (int s = s0; s < s1; ++s) {
+            // this wave's copies of step s have landed and its reads of step s-1 are done; then all meet
+            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            if (s + 1 < s1) issue(s + 1, (s + 1 - s0) & 1);
+#pragma unroll
+            for (int ks = 0; ks < kBK / 32; ++ks) {
+                read((s - s0) & 1, ks);
+                multiply();
+            }
+        }
     }
 
     // ---- epilogue.  Lane (lr, lg) of MFMA tile (i, j) holds columns 4 lg .. 4 lg + 3 of row lr.  The
     // wave's tile goes through LDS (64 rows at a time, 16-byte chunk c of row r at c ^ (r & 15 or 7)) so
     // that 8 or 16 neighbouring lanes take one row: whole lines are read and written, and the
     // epilogue's code appears once.
-    if constexpr (std::is_same_v<Epi, EpiPartial<PAIR>>) epi.part += (size_t)sp * epi.plane * (PAIR ? 2 : 1);
     constexpr int kCh = 4 * TC;                              // 16-byte chunks of a float32 row of the wave's tile
     constexpr int kJP = TR < 4 ? TR : 4;                     // MFMA tile rows per pass
     constexpr int kLanes = PAIR ? kCh / 2 : kCh, kRows = 64 / kLanes;
+    constexpr int U = 4;                                     // row groups handled together
     static_assert(NW * kJP * 16 * kCh * 16 <= 2 * kStage, "the passes fit in the operands' LDS");
     static_assert(kCh == 8 || kCh == 16, "chunk permutation");
+    static_assert(kJP * 16 % (kRows * U) == 0, "whole groups");
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");    // every wave has read its last operands
     unsigned char *mine = smem + wave * (kJP * 16 * kCh * 16);
     const int ec = lane % kLanes, er = lane / kLanes;
     const int c = c0 + wc * (PAIR ? kHalf : kWCols) + 4 * ec;
-    f32x4 sa = {0.f, 0.f, 0.f, 0.f}, sb = {0.f, 0.f, 0.f, 0.f};
+    const bool live_c = c < p.C;
+    typename Epi::Cols cols = epi.cols(live_c ? c : 0);
+    float *ptile = ga.part + (size_t)((slot - ga.full) * ga.split + sp) * (BR * BC) + (c - c0);
+    f32x4 sa = kZero4, sb = kZero4;
     static_for<TR / kJP>([&](auto pass) {
 #pragma unroll
         for (int j = 0; j < kJP; ++j)
@@ -260,27 +317,35 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const
             for (int i = 0; i < TC; ++i)
                 *(f32x4 *)(mine + (16 * j + lr) * (kCh * 16) + (((4 * i + lg) ^ (lr & (kCh - 1))) << 4)) =
                     acc[i][pass * kJP + j];
-#pragma unroll 2
-        for (int it = 0; it < kJP * 16 / kRows; ++it) {
-            const int row = it * kRows + er;
-            const int r = r0 + wr * 16 * TR + pass * kJP * 16 + row;
-            if (r < p.R && c < p.C) {
+#pragma unroll 1
+        for (int it = 0; it < kJP * 16 / kRows; it += U) {
+            const int row0 = it * kRows + er;                // rows row0 + u * kRows of the pass
+            const int lrow = wr * 16 * TR + pass * kJP * 16 + row0, r = r0 + lrow;
+            f32x4 a[U], b[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int row = row0 + u * kRows;
                 const unsigned char *src = mine + row * (kCh * 16);
-                const f32x4 a = *(const f32x4 *)(src + ((ec ^ (row & (kCh - 1))) << 4));
-                f32x4 b = a;
-                if constexpr (PAIR) b = *(const f32x4 *)(src + (((ec + kLanes) ^ (row & (kCh - 1))) << 4));
-                f32x4 ca = {0.f, 0.f, 0.f, 0.f}, cb = {0.f, 0.f, 0.f, 0.f};
-                epi.apply(r, c, a, b, ca, cb);
-                if constexpr (Epi::kColSum) {
-                    sa += ca;
-                    sb += cb;
+                a[u] = *(const f32x4 *)(src + ((ec ^ (row & (kCh - 1))) << 4));
+                if constexpr (PAIR) b[u] = *(const f32x4 *)(src + (((ec + kLanes) ^ (row & (kCh - 1))) << 4));
+            }
+            if (!live_c || r >= p.R) continue;
+            if (split_tile) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (r + u * kRows >= p.R) continue;
+                    float *dst = ptile + (lrow + u * kRows) * BC;
+                    *(f32x4 *)dst = a[u];
+                    if constexpr (PAIR) *(f32x4 *)(dst + kPairCols) = b[u];
                 }
+            } else {
+                epi.rows(cols, r, kRows, p.R, c, a, b, sa, sb);
             }
         }
     });
     if constexpr (Epi::kColSum) {
-        if (epi.cs) {
-            // the wave's 16 TR rows: one partial row per wave row of the grid
+        if (epi.cs && !split_tile) {
+            // the wave's 16 TR rows: cs_sub partial rows, the first with the sum
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -288,44 +353,37 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const
                     sa[q] += __shfl_xor(sa[q], o, kWave);
                     if constexpr (PAIR) sb[q] += __shfl_xor(sb[q], o, kWave);
                 }
-            if (er == 0 && c < p.C) {
-                float *row = epi.cs + (size_t)(tr * Cfg::WR + wr) * epi.csld;
-                *(f32x4 *)(row + c) = sa;
-                if constexpr (PAIR) *(f32x4 *)(row + p.C + c) = sb;
+            if (live_c) {
+                float *row = epi.cs + (size_t)((tr * Cfg::WR + wr) * ga.cs_sub) * epi.csld;
+                for (int i = er; i < ga.cs_sub; i += kRows) {
+                    *(f32x4 *)(row + (size_t)i * epi.csld + c) = i ? kZero4 : sa;
+                    if constexpr (PAIR) *(f32x4 *)(row + (size_t)i * epi.csld + p.C + c) = i ? kZero4 : sb;
+                }
             }
         }
     }
 }
 
+// The product with its epilogue, and the sum of its split tiles.
 template <class Cfg, int FORM, class Epi>
-moe_status dense_launch_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &e, hipStream_t s) {
+moe_status dense_run_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s) {
     constexpr int lds = 2 * (Cfg::BR + Cfg::BC) * kBK * 2;
-    GemmArgs ga{p, pl.tr, pl.tc, pl.split, pl.steps, (p.K + kBK - 1) / kBK};
-    auto kern = dense_gemm_kernel<Cfg, FORM, Epi>;
-    hipLaunchKernelGGL(kern, dim3((unsigned)(pl.tr * pl.tc * pl.split)), dim3(64 * Cfg::WR * Cfg::WC), lds, s, ga, e);
-    return launch_check("dense product");
+    const int tiles = pl.tr * pl.tc;
+    const bool tail = pl.full < tiles;
+    GemmArgs ga{p, pl.tr, pl.tc, pl.full, pl.split, pl.steps, (p.K + kBK - 1) / kBK, tail ? Cfg::BR / Cfg::WR / kFinishRows : 1,
+                part};
+    hipLaunchKernelGGL((dense_gemm_kernel<Cfg, FORM, Epi>), dim3((unsigned)(pl.full + (tiles - pl.full) * pl.split)),
+                       dim3(64 * Cfg::WR * Cfg::WC), lds, s, ga, e);
+    MOE_TRY(launch_check("dense product"));
+    return tail ? dense_finish(p, pl, Cfg::BR, Cfg::BC, e, part, s) : MOE_OK;
 }
 
-template <int FORM, class Epi>
-moe_status dense_launch(const DenseProduct &p, const DensePlan &pl, const Epi &e, hipStream_t s) {
-    if (pl.cfg == 0) return dense_launch_cfg<CfgL, FORM, Epi>(p, pl, e, s);
-    if constexpr (FORM != kFormTN)
-        if (pl.cfg == 2) return dense_launch_cfg<CfgS, FORM, Epi>(p, pl, e, s);
-    return dense_launch_cfg<CfgM, FORM, Epi>(p, pl, e, s);
-}
-
-// The product with its epilogue: in one kernel, or as parts summed by a second one.
 template <int FORM, class Epi>
 moe_status dense_run(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s) {
-    if (pl.split * p.terms == 1) return dense_launch<FORM>(p, pl, e, s);
-    const int ld = (p.C + 3) & ~3;
-    EpiPartial<Epi::kPair> ep;
-    ep.part = part;
-    ep.plane = (size_t)p.R * ld;
-    ep.ld = ld;
-    MOE_TRY((dense_launch<FORM>(p, pl, ep, s)));
-    // a part's terms lie one after the other, like further parts
-    return dense_finish(pl.split * p.terms, e, part, p.R / p.terms, p.C, s);
+    if (pl.cfg == 0) return dense_run_cfg<CfgL, FORM>(p, pl, e, part, s);
+    if constexpr (FORM != kFormTN)
+        if (pl.cfg == 2) return dense_run_cfg<CfgS, FORM>(p, pl, e, part, s);
+    return dense_run_cfg<CfgM, FORM>(p, pl, e, part, s);
 }
 
 }  // namespace moe

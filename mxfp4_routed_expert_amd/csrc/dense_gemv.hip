@@ -111,15 +111,15 @@ __global__ __launch_bounds__(64 * kWaves) void dense_gemv_kernel(const void *__r
     __syncthreads();
     const int t = threadIdx.x;
     if (t < T) {
-        f32x4 v[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        f32x4 a[1] = {kZero4}, b[1] = {kZero4}, ca, cb;
 #pragma unroll
-        for (int m = 0; m < NM; ++m)
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) v[m][q] += s_sum[w][(4 * m + q) * MT + t];
-        f32x4 ca, cb;
-        epi.apply(t, c, v[0], v[1], ca, cb);
+            for (int w = 0; w < kWaves; ++w) {
+                a[0][q] += s_sum[w][q * MT + t];
+                if constexpr (NM == 2) b[0][q] += s_sum[w][(4 + q) * MT + t];
+            }
+        epi.rows(epi.cols(c), t, 1, T, c, a, b, ca, cb);
     }
 }
 
