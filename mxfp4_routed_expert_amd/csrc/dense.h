@@ -412,7 +412,7 @@ struct DenseProduct {
 // the epilogue in the product kernel; the sum of each of the rest is split into `split` parts over
 // workgroups of the same launch, whose float32 results a second kernel adds up, in order, and finishes.
 struct DensePlan {
-    int cfg;              // 0: 256 x 256, 1: 128 x 128, 2: 64 x 128 tiles
+    int cfg;              // tile shape: 0 L, 1 M, 2 S, 3 D (dense_gemm.h)
     int tr, tc;           // tiles along rows and columns
     int full, split;
     int steps;            // 64-value steps of the sum, all segments

@@ -22,11 +22,25 @@
 
 namespace moe {
 
-struct CfgL { static constexpr int BR = 256, BC = 256, WR = 2, WC = 4; static constexpr bool kAlternate = true; };    // 8 waves of 128 x 64
-struct CfgM { static constexpr int BR = 128, BC = 128, WR = 2, WC = 2; static constexpr bool kAlternate = false; };   // 4 waves of 64 x 64
-struct CfgS { static constexpr int BR = 64, BC = 128, WR = 1, WC = 4; static constexpr bool kAlternate = false; };    // 4 waves of 64 x 32
+struct CfgL {                // 8 waves of 128 x 64, alternating
+    static constexpr int BR = 256, BC = 256, WR = 2, WC = 4, kStages = 2;
+    static constexpr bool kAlternate = true;
+};
+struct CfgM {                // 4 waves of 64 x 64, two workgroups a CU: one's start and end beside the other's products
+    static constexpr int BR = 128, BC = 128, WR = 2, WC = 2, kStages = 2;
+    static constexpr bool kAlternate = false;
+};
+struct CfgS {                // 4 waves of 64 x 32, two workgroups a CU
+    static constexpr int BR = 64, BC = 128, WR = 1, WC = 4, kStages = 3;
+    static constexpr bool kAlternate = false;
+};
+struct CfgD {                // as M with a step more in flight, one workgroup a CU
+    static constexpr int BR = 128, BC = 128, WR = 2, WC = 2, kStages = 3;
+    static constexpr bool kAlternate = false;
+};
 
 constexpr int kBK = 64;
+#define MOE_INLINE __attribute__((always_inline))
 
 struct GemmArgs {
     DenseProduct p;
@@ -38,18 +52,22 @@ struct GemmArgs {
 __device__ __attribute__((aligned(16))) const uint32_t g_dense_zero[4] = {0, 0, 0, 0};
 
 // global -> LDS copies, 16 bytes a lane, to dst + 16 lane (asm: the compiler would otherwise wait for
-// all copies in flight before every LDS read; the loop waits for exactly what it needs).
+// all copies in flight before every LDS read; the loop waits for exactly what it needs; the s_nop is the
+// wait state between a write of M0 and its use by a copy).
 MOE_DEV void copy16(const void *base, uint32_t voff, uint32_t lds) {
-    asm volatile("global_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" ::"v"(voff), "s"(base), "{m0}"(lds) : "memory");
 }
 MOE_DEV void copy16_addr(const void *src, uint32_t lds) {
-    asm volatile("global_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(lds) : "memory");
+    asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(src), "{m0}"(lds) : "memory");
 }
 MOE_DEV const uint16_t *uniform16(const uint16_t *q) {
     const uint64_t v = (uint64_t)(uintptr_t)q;
     const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
     return (const uint16_t *)(uintptr_t)(((uint64_t)hi << 32) | lo);
 }
+
+// (by value: a choice between captured variables would put them all in scratch memory)
+MOE_DEV const uint16_t *pick(int i, const uint16_t *a, const uint16_t *b, const uint16_t *c) { return i == 0 ? a : (i == 1 ? b : c); }
 
 MOE_DEV int ks_swz(int k) { return ((k & 3) | (((k >> 3) & 1) << 2)) << 1; }
 
@@ -74,7 +92,7 @@ struct Operand {
 };
 
 template <class Cfg, int FORM, class Epi>
-__global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const GemmArgs ga, Epi epi) {
+__global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, 2) void dense_gemm_kernel(const GemmArgs ga, Epi epi) {
     constexpr int BR = Cfg::BR, BC = Cfg::BC, NW = Cfg::WR * Cfg::WC;
     constexpr int TR = BR / Cfg::WR / 16, TC = BC / Cfg::WC / 16;
     constexpr bool RS = FORM == kFormTN, CS = FORM != kFormNT, PAIR = Epi::kPair;
@@ -126,8 +144,8 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const
     // pair tile: LDS row j of the columns operand is, within wave wc's 16 TC rows, gate column
     // j % (8 TC) in the first half and up column in the second
     constexpr int kWCols = 16 * TC, kHalf = 8 * TC;
-    auto pair_mat = [&](int row) { return (row % kWCols) / kHalf; };
-    auto pair_col = [&](int row) { return row / kWCols * kHalf + row % kHalf; };
+    auto pair_mat = [&](int row) MOE_INLINE { return (row % kWCols) / kHalf; };
+    auto pair_col = [&](int row) MOE_INLINE { return row / kWCols * kHalf + row % kHalf; };
 #pragma unroll
     for (int t = 0; t < OpC::kCopies; ++t) {
         if constexpr (!CS) {
@@ -141,45 +159,66 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const
     }
 
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)smem);
-    // copies of step s into stage st
-    auto issue = [&](int s, int st) {
-        const int seg = s / ga.seg_steps, k0 = (s - seg * ga.seg_steps) * kBK;
-        const uint16_t *rb = seg == 0 ? p.rp[0] : (seg == 1 ? p.rp[1] : p.rp[2]);
-        const uint16_t *cb = PAIR ? p.cp[0] : (seg == 0 ? p.cp[0] : (seg == 1 ? p.cp[1] : p.cp[2]));
+    // Copies of the next step (s0, s0 + 1, ... in order) into stage st.  The sources advance by a constant per
+    // step and start over at a segment's end; all of it stays in scalar registers (a division per step in
+    // their place cost more than the step's matrix instructions).
+    int seg = s0 / ga.seg_steps;
+    int live = p.K - (s0 - seg * ga.seg_steps) * kBK;        // values of the sum left in the segment
+    const uint16_t *rb, *cb, *ub = nullptr;
+    // (held in registers: a reload of the arguments inside the loop would make every LDS wait a full one)
+    const uint16_t *rp0 = uniform16(p.rp[0]), *rp1 = uniform16(p.rp[1]), *rp2 = uniform16(p.rp[2]);
+    const uint16_t *cp0 = uniform16(p.cp[0]), *cp1 = uniform16(p.cp[1]), *cp2 = uniform16(p.cp[2]);
+    auto sources = [&](int k0) MOE_INLINE {
+        rb = pick(seg, rp0, rp1, rp2);
+        cb = pick(PAIR ? 0 : seg, cp0, cp1, cp2);
         rb += RS ? (size_t)k0 * p.ldr + r0 : (size_t)r0 * p.ldr + k0;
         cb += CS ? (size_t)k0 * p.ldc + c0 : (size_t)c0 * p.ldc + k0;
-        const uint16_t *ub = PAIR ? p.cp[1] + ((size_t)c0 * p.ldc + k0) : nullptr;
-        const uint32_t lr_ = lds0 + st * kStage + OpR::slot(wave, 0) * 1024;
-        const uint32_t lc_ = lds0 + st * kStage + OpR::kBytes + OpC::slot(wave, 0) * 1024;
-        const int live = p.K - k0;                           // values of the sum left in this segment
-        if (live >= kBK) {
-            const uint16_t *rbu = uniform16(rb);
-#pragma unroll
-            for (int t = 0; t < OpR::kCopies; ++t) copy16(rbu, opr.voff[t], lr_ + t * 1024);
-#pragma unroll
-            for (int t = 0; t < OpC::kCopies; ++t) {
-                const uint16_t *b = cb;
-                if constexpr (PAIR) b = pair_mat(OpC::slot(wave, t) * 8) ? ub : cb;
-                copy16(uniform16(b), opc.voff[t], lc_ + t * 1024);
-            }
+        if constexpr (PAIR) ub = cp1 + (size_t)c0 * p.ldc + k0;
+    };
+    sources(p.K - live);
+    const size_t radv = RS ? (size_t)kBK * p.ldr : kBK, cadv = CS ? (size_t)kBK * p.ldc : kBK;
+    // copy t (the rows operand's, then the columns operand's) into stage st; tail: the segment's last, partial step
+    constexpr int kPer = OpR::kCopies + OpC::kCopies;
+    auto piece = [&](auto tt, int st, auto tail) MOE_INLINE {
+        constexpr int t = decltype(tt)::value;
+        constexpr bool R = t < OpR::kCopies;
+        constexpr int u = R ? t : t - OpR::kCopies;
+        const uint32_t at = lds0 + st * kStage + (R ? OpR::slot(wave, u) * 1024 : OpR::kBytes + OpC::slot(wave, u) * 1024);
+        uint32_t off;
+        const uint16_t *b;
+        int k;
+        if constexpr (R) {
+            off = opr.voff[u];
+            b = rb;
+            k = RS ? OpR::ks_k(wave, u, lane) : 8 * OpR::kc_chunk(OpR::kc_row(wave, u, lane), lane);
         } else {
-#pragma unroll
-            for (int t = 0; t < OpR::kCopies; ++t) {
-                const int row = OpR::kc_row(wave, t, lane);
-                const int k = RS ? OpR::ks_k(wave, t, lane) : 8 * OpR::kc_chunk(row, lane);
-                const void *a = (const char *)rb + opr.voff[t];
-                copy16_addr(k < live ? a : (const void *)g_dense_zero, lr_ + t * 1024);
-            }
-#pragma unroll
-            for (int t = 0; t < OpC::kCopies; ++t) {
-                const int row = OpC::kc_row(wave, t, lane);
-                const int k = CS ? OpC::ks_k(wave, t, lane) : 8 * OpC::kc_chunk(row, lane);
-                const uint16_t *b = cb;
-                if constexpr (PAIR) b = pair_mat(OpC::slot(wave, t) * 8) ? ub : cb;
-                const void *a = (const char *)b + opc.voff[t];
-                copy16_addr(k < live ? a : (const void *)g_dense_zero, lc_ + t * 1024);
-            }
+            off = opc.voff[u];
+            b = PAIR ? pick(pair_mat(OpC::slot(wave, u) * 8), cb, ub, ub) : cb;
+            k = CS ? OpC::ks_k(wave, u, lane) : 8 * OpC::kc_chunk(OpC::kc_row(wave, u, lane), lane);
         }
+        if constexpr (decltype(tail)::value) {
+            const void *a = (const char *)b + off;
+            copy16_addr(k < live ? a : (const void *)g_dense_zero, at);
+        } else {
+            copy16(uniform16(b), off, at);
+        }
+    };
+    auto advance = [&]() MOE_INLINE {
+        live -= kBK;
+        if (live > 0) {
+            rb += radv;
+            cb += cadv;
+            if constexpr (PAIR) ub += cadv;
+        } else if (seg + 1 < p.nseg) {
+            ++seg;
+            live = p.K;
+            sources(0);
+        }
+    };
+    auto issue = [&](int st) MOE_INLINE {
+        if (live >= kBK) static_for<kPer>([&](auto t) MOE_INLINE { piece(t, st, std::false_type{}); });
+        else static_for<kPer>([&](auto t) MOE_INLINE { piece(t, st, std::true_type{}); });
+        advance();
     };
 
     f32x4 acc[TC][TR];
@@ -191,11 +230,11 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const
     typedef short s16x4 __attribute__((ext_vector_type(4)));
     typedef short s16x8 __attribute__((ext_vector_type(8)));
     // MFMA operand of free indices f0 .. f0+15 (f0 a multiple of 16), values 32 ks + 8 lg .. +7
-    auto frag_c = [&](int base, int f0, int ks) {            // contiguous
+    auto frag_c = [&](int base, int f0, int ks) MOE_INLINE {            // contiguous
         const int at = base + f0 * 128 + lr * 128 + (((4 * ks + lg) ^ (lr >> 1)) << 4);
         return *(const bf16x8 *)(smem + at);
     };
-    auto frag_s = [&](int base, int f0, int ks, auto width) { // strided
+    auto frag_s = [&](int base, int f0, int ks, auto width) MOE_INLINE { // strided
         constexpr int W = decltype(width)::value;            // free indices of the tile
         const int k = 32 * ks + 8 * lg + (lr >> 2);
         const int chunk = ((f0 >> 3) + ((lr & 3) >> 1)) ^ ks_swz(k);
@@ -206,88 +245,202 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const
         const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
         return __builtin_bit_cast(bf16x8, v);
     };
-    bf16x8 fr[TR], fc[TC];
-    auto read = [&](int st, int ks) {
+    struct Frags {
+        bf16x8 r[TR], c[TC];
+    };
+    auto read = [&](Frags &f, int st, int ks) MOE_INLINE {
         const int base_r = st * kStage, base_c = st * kStage + OpR::kBytes;
 #pragma unroll
         for (int j = 0; j < TR; ++j) {
             const int f0 = wr * 16 * TR + 16 * j;
-            if constexpr (RS) fr[j] = frag_s(base_r, f0, ks, std::integral_constant<int, BR>{});
-            else fr[j] = frag_c(base_r, f0, ks);
+            if constexpr (RS) f.r[j] = frag_s(base_r, f0, ks, std::integral_constant<int, BR>{});
+            else f.r[j] = frag_c(base_r, f0, ks);
         }
 #pragma unroll
         for (int i = 0; i < TC; ++i) {
             const int f0 = wc * 16 * TC + 16 * i;
-            if constexpr (CS) fc[i] = frag_s(base_c, f0, ks, std::integral_constant<int, BC>{});
-            else fc[i] = frag_c(base_c, f0, ks);
+            if constexpr (CS) f.c[i] = frag_s(base_c, f0, ks, std::integral_constant<int, BC>{});
+            else f.c[i] = frag_c(base_c, f0, ks);
         }
     };
-    auto multiply = [&]() {
-#pragma unroll
-        for (int i = 0; i < TC; ++i)
-#pragma unroll
-            for (int j = 0; j < TR; ++j)
-                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fc[i], fr[j], acc[i][j], 0, 0, 0);
+    // The products of one half step, with the whole copies P0 .. P1-1 into stage st spread between them: a copy
+    // occupies the CU's address unit for 16 cycles, and a wave that issues one after another waits for it
+    // instead of multiplying.
+    using Zero = std::integral_constant<int, 0>;
+    using Half = std::integral_constant<int, kPer / 2>;
+    using All = std::integral_constant<int, kPer>;
+    auto multiply_copy = [&](const Frags &f, auto p0, auto p1, int st) MOE_INLINE {
+        constexpr int n = decltype(p1)::value - decltype(p0)::value, every = TC * TR / (n > 0 ? n : 1);
+        static_assert(n == 0 || every >= 1, "a copy between products");
+        static_for<TC * TR>([&](auto m) MOE_INLINE {
+            constexpr int i = m / TR, j = m % TR;
+            if constexpr (n > 0 && m % every == 0 && m / every < n) {
+                __builtin_amdgcn_sched_barrier(0);
+                piece(std::integral_constant<int, decltype(p0)::value + m / every>{}, st, std::false_type{});
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.c[i], f.r[j], acc[i][j], 0, 0, 0);
+        });
+    };
+    auto multiply = [&](const Frags &f) MOE_INLINE { multiply_copy(f, Zero{}, Zero{}, 0); };
+    // Most steps' copies are whole ones of the current segment.  They run in loops without a branch, whose
+    // instructions all fit beside the matrix instructions; a step at a segment's end, or with nothing more to copy,
+    // runs by itself.
+    auto next_source = [&]() MOE_INLINE {
+        rb += radv;
+        cb += cadv;
+        if constexpr (PAIR) ub += cadv;
+    };
+    auto whole_steps = [&](int most) MOE_INLINE { return max(0, min(most, live / kBK)); };
+    auto whole_done = [&](int n) MOE_INLINE {
+        live -= n * kBK;
+        if (n > 0 && live <= 0 && seg + 1 < p.nseg) {
+            ++seg;
+            live = p.K;
+            sources(0);
+        }
     };
 
     if constexpr (Cfg::kAlternate) {
         // Two waves share a SIMD: wave w of the first half of the workgroup and w + NW/2 of the second.  While
         // one multiplies (32 matrix instructions), the other reads its next operands from LDS, then they
         // change places at a barrier: the matrix cores never wait for an LDS read.  The second half runs one
-        // phase behind.  A step is four phases of a wave: read, multiply, read, multiply.  Step s+1's copies go
-        // out in the first one (its buffer was last read, by the second half, in the phase before) and have
-        // landed when the first half reads them four phases later.
-        const bool second = wave >= NW / 2;
-        auto phase_end = [&]() {
+        // phase behind.  A step is four phases of a wave: read, multiply, read, multiply; numbered from the
+        // first half's, step s reads its buffer in phases 4s .. 4s + 3 (the last one is the second half's).
+        // Step s + 1's copies into the other buffer go out between matrix instructions, the second half's in
+        // phase 4s (its last of step s - 1), the first half's in 4s + 1, and have landed at the end of 4s + 3.
+        auto phase_end = [&]() MOE_INLINE {
+            __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_sched_barrier(0);
             asm volatile("s_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
         };
-        auto read_end = [&]() {
+        auto read_end = [&]() MOE_INLINE {
             __builtin_amdgcn_sched_barrier(0);
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(1);
         };
-        auto copies_end = [&]() {
+        auto copies_end = [&]() MOE_INLINE {                 // (also a read's or a multiplication's end)
+            __builtin_amdgcn_s_setprio(0);
             __builtin_amdgcn_sched_barrier(0);
             asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
             __builtin_amdgcn_sched_barrier(0);
+        };
+        Frags f;
+        auto run = [&](auto second) MOE_INLINE {
+            constexpr bool S2 = decltype(second)::value;
+            // one step: with COPY, the whole copies of step s + 1 (first half) or s + 2 (second half)
+            auto step = [&](int s, auto copy) MOE_INLINE {
+                constexpr bool COPY = decltype(copy)::value;
+                const int st = (s - s0) & 1;
+                read(f, st, 0);
+                read_end();
+                if constexpr (COPY && !S2) multiply_copy(f, Zero{}, All{}, st ^ 1);
+                else multiply(f);
+                phase_end();
+                read(f, st, 1);
+                if constexpr (S2) {
+                    copies_end();
+                    __builtin_amdgcn_s_setprio(1);
+                } else {
+                    read_end();
+                }
+                if constexpr (COPY && S2) multiply_copy(f, Zero{}, All{}, st);
+                else multiply(f);
+                if constexpr (S2) phase_end();
+                else copies_end();
+                if constexpr (COPY) next_source();
+            };
+            constexpr int kAhead = S2 ? 2 : 1;
+            if (S2) {
+                if (s0 + 1 < s1) issue(1);
+                phase_end();
+            }
+            int s = s0;
+            while (s < s1) {
+                const int n = whole_steps(s1 - kAhead - s);
+                for (int i = 0; i < n; ++i, ++s) step(s, std::true_type{});
+                whole_done(n);
+                if (s >= s1) break;
+                // a step whose copies are the segment's partial step, or none (they go out at its start, or, the second
+                // half's, once it has read its last operands)
+                const int st = (s - s0) & 1;
+                if (!S2 && s + 1 < s1) issue(st ^ 1);
+                read(f, st, 0);
+                read_end();
+                multiply(f);
+                phase_end();
+                read(f, st, 1);
+                if constexpr (S2) copies_end();
+                else read_end();
+                if (S2 && s + 2 < s1) issue(st);
+                multiply(f);
+                if constexpr (S2) phase_end();
+                else copies_end();
+                ++s;
+            }
+            if (!S2) phase_end();
         };
         if (s0 < s1) {
-            issue(s0, 0);
+            issue(0);
             copies_end();
-            if (second) phase_end();
-            for (int s = s0; s < s1; ++s) {
-                const int st = (s - s0) & 1;
-                if (s + 1 < s1) issue(s + 1, st ^ 1);
-                read(st, 0);
-                read_end();
-                __builtin_amdgcn_s_setprio(1);
-                multiply();
-                __builtin_amdgcn_s_setprio(0);
-                phase_end();
-                read(st, 1);
-                if (second) copies_end();
-                else read_end();
-                __builtin_amdgcn_s_setprio(1);
-                multiply();
-                __builtin_amdgcn_s_setprio(0);
-                if (second) phase_end();
-                else copies_end();
-            }
-            if (!second) phase_end();
+            if (wave >= NW / 2) run(std::true_type{});
+            else run(std::false_type{});
         }
     } else {
-        if (s0 < s1) issue(s0, 0);
-        for (int s = s0; s < s1; ++s) {
-            // this wave's copies of step s have landed and its reads of step s-1 are done; then all meet
-            asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-            if (s + 1 < s1) issue(s + 1, (s + 1 - s0) & 1);
+        // Operands are read one 32-value half step ahead of the products that use them, so reads and matrix
+        // instructions overlap.  After the barrier in the middle of step s every operand of it has been read:
+        // its buffer is free, and the copies of step s + kStages go into it, between the matrix instructions of
+        // the two half steps that follow.
+        constexpr int kStages = Cfg::kStages;
+        static_assert(kPer * (kStages - 2) < 64, "the wait counter's range");
+        auto landed = [&](bool newer) MOE_INLINE {           // the oldest step's copies, then all waves meet
+            if (newer) asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(kPer * (kStages - 2)) : "memory");
+            else asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        };
+        // (tells the compiler that the older operands are there, so that it waits for no newer one)
+        auto reads_done = [&]() MOE_INLINE { __builtin_amdgcn_s_waitcnt(0xc07f); };
+        if (s0 < s1) {
+            Frags f0, f1;
 #pragma unroll
-            for (int ks = 0; ks < kBK / 32; ++ks) {
-                read((s - s0) & 1, ks);
-                multiply();
+            for (int i = 0; i < kStages - 1; ++i)
+                if (s0 + i < s1) issue(i);
+            landed(s0 + kStages - 1 <= s1);
+            if (s0 + kStages - 1 < s1) issue(kStages - 1);
+            read(f0, 0, 0);
+            read(f1, 0, 1);
+            multiply(f0);
+            // from the middle of step s to the middle of step s + 1
+            int st = 0;
+            auto step = [&](int s, auto copy) MOE_INLINE {
+                constexpr bool COPY = decltype(copy)::value;
+                landed(COPY || s + kStages <= s1);
+                const int free = st;
+                st = st + 1 == kStages ? 0 : st + 1;
+                if (!COPY && s + kStages < s1) issue(free);
+                reads_done();
+                read(f0, st, 0);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (COPY) multiply_copy(f1, Zero{}, Half{}, free);
+                else multiply(f1);
+                __builtin_amdgcn_sched_barrier(0);
+                reads_done();
+                read(f1, st, 1);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (COPY) multiply_copy(f0, Half{}, All{}, free);
+                else multiply(f0);
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (COPY) next_source();
+            };
+            int s = s0;
+            while (s + 1 < s1) {
+                const int n = whole_steps(s1 - kStages - s);
+                for (int i = 0; i < n; ++i, ++s) step(s, std::true_type{});
+                whole_done(n);
+                if (s + 1 < s1) step(s++, std::false_type{});
             }
+            multiply(f1);
         }
     }
 
@@ -299,7 +452,7 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const
     constexpr int kJP = TR < 4 ? TR : 4;                     // MFMA tile rows per pass
     constexpr int kLanes = PAIR ? kCh / 2 : kCh, kRows = 64 / kLanes;
     constexpr int U = 4;                                     // row groups handled together
-    static_assert(NW * kJP * 16 * kCh * 16 <= 2 * kStage, "the passes fit in the operands' LDS");
+    static_assert(NW * kJP * 16 * kCh * 16 <= Cfg::kStages * kStage, "the passes fit in the operands' LDS");
     static_assert(kCh == 8 || kCh == 16, "chunk permutation");
     static_assert(kJP * 16 % (kRows * U) == 0, "whole groups");
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");    // every wave has read its last operands
@@ -367,7 +520,7 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC) void dense_gemm_kernel(const
 // The product with its epilogue, and the sum of its split tiles.
 template <class Cfg, int FORM, class Epi>
 moe_status dense_run_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s) {
-    constexpr int lds = 2 * (Cfg::BR + Cfg::BC) * kBK * 2;
+    constexpr int lds = Cfg::kStages * (Cfg::BR + Cfg::BC) * kBK * 2;
     const int tiles = pl.tr * pl.tc;
     const bool tail = pl.full < tiles;
     GemmArgs ga{p, pl.tr, pl.tc, pl.full, pl.split, pl.steps, (p.K + kBK - 1) / kBK, tail ? Cfg::BR / Cfg::WR / kFinishRows : 1,
@@ -381,6 +534,7 @@ moe_status dense_run_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &
 template <int FORM, class Epi>
 moe_status dense_run(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s) {
     if (pl.cfg == 0) return dense_run_cfg<CfgL, FORM>(p, pl, e, part, s);
+    if (pl.cfg == 3) return dense_run_cfg<CfgD, FORM>(p, pl, e, part, s);
     if constexpr (FORM != kFormTN)
         if (pl.cfg == 2) return dense_run_cfg<CfgS, FORM>(p, pl, e, part, s);
     return dense_run_cfg<CfgM, FORM>(p, pl, e, part, s);
