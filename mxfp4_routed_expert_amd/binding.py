@@ -7,7 +7,6 @@ module raises: there is no fallback.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import os
@@ -568,35 +567,42 @@ def moe_mx_quantize(x):
 
 # ------------------------------------------------------------------ dense bf16 layers
 
-@contextlib.contextmanager
-def _switched(index):
-    with torch.cuda.device(index):
-        yield
-
-
-def _on(x):
-    """The device of x as the current device for a call (its current stream is then the one used)."""
-    i = x.device.index
-    return _switched(i) if i != torch.cuda.current_device() else _HERE_ALREADY
-
-
-_HERE_ALREADY = contextlib.nullcontext()
-
-
 def _operands(dev, *items):
-    """items: (tensor or None, dtype or tuple of dtypes, name, shape).  All on `dev`, contiguous, 16-byte aligned."""
+    """items: (tensor or None, dtype or tuple of dtypes, name, shape or None).  Each on `dev`, of its dtype and shape,
+    contiguous.  (One expression a tensor when all is well: a decoded token's call is a few microseconds.)"""
     for t, dtype, name, shape in items:
-        if t is None:
+        if t is None or (isinstance(t, torch.Tensor) and (t.dtype is dtype) and t.device == dev and t.is_contiguous()
+                         and (shape is None or t.shape == shape)):
             continue
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
         if isinstance(dtype, tuple):
-            if t.dtype not in dtype:
+            if isinstance(t, torch.Tensor) and t.dtype not in dtype:
                 raise TypeError(f"{name} must be one of {dtype} (got {t.dtype})")
             dtype = None
         _need(t, dtype, name, shape)
         if t.device != dev:
             raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, stream) on dev's current stream, with dev the current device for the call."""
+    i = dev.index
+    if i == torch.cuda.current_device():
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    else:
+        with torch.cuda.device(i):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(i))
+    if status != MOE_OK:
+        check(status)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _one_of(t, types):
+    """t's dtype when it is one of `types`, else `types` (refused by _operands)."""
+    dt = getattr(t, "dtype", None)
+    return dt if dt in types else tuple(types)
 
 
 def _matrix(t, name):
@@ -616,8 +622,8 @@ def _act_fn(name):
 @functools.lru_cache(maxsize=4096)
 def _dense_plan(kind, *sizes):
     """(descriptor, workspace bytes) of a dense call: a function of its sizes and types alone."""
-    d = (LinearDesc if kind.startswith("linear") else GateupDesc)(*sizes)
-    return d, getattr(lib, f"moe_dense_{kind}_workspace")(ctypes.byref(d))
+    d = ctypes.byref((LinearDesc if kind.startswith("linear") else GateupDesc)(*sizes))
+    return d, getattr(lib, f"moe_dense_{kind}_workspace")(d)
 
 
 def moe_dense_linear_workspace(T, n, kdim, act_fn="none", x_dtype=torch.bfloat16, out_dtype=torch.bfloat16):
@@ -640,9 +646,8 @@ def _ws_for(ws, need, dev):
     if need == 0:
         return None, 0
     if ws is None:
-        ws = _workspace(need, dev)
-    else:
-        _operands(dev, (ws, torch.uint8, "ws", None))
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
+    _operands(dev, (ws, torch.uint8, "ws", None))
     return ws, ws.numel()
 
 
@@ -655,14 +660,12 @@ def moe_dense_linear(x, w, bias=None, act_fn="none", residual=None, out=None, ou
     if dt not in DT:
         raise TypeError(f"y must be bfloat16 or float32 (got {dt})")
     dev = x.device
-    _operands(dev, (x, tuple(DT), "x", None), (w, torch.bfloat16, "w", (n, kdim)), (bias, torch.float32, "bias", (n,)),
+    _operands(dev, (x, _one_of(x, DT), "x", None), (w, torch.bfloat16, "w", (n, kdim)), (bias, torch.float32, "bias", (n,)),
               (residual, dt, "residual", (T, n)), (out, dt, "out", (T, n)))
     d, need = _dense_plan("linear", T, n, kdim, _act_fn(act_fn), DT[x.dtype], DT[dt], 0)
-    with _on(x):
-        y = out if out is not None else torch.empty((T, n), dtype=dt, device=dev)
-        ws, nws = _ws_for(ws, need, dev)
-        check(lib.moe_dense_linear(ctypes.byref(d), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y), _ptr(ws), nws,
-                                   _stream()))
+    y = out if out is not None else torch.empty((T, n), dtype=dt, device=dev)
+    ws, nws = _ws_for(ws, need, dev)
+    _launch(dev, lib.moe_dense_linear, d, _at(x), _at(w), _at(bias), _at(residual), _at(y), _at(ws), nws)
     return y
 
 
@@ -677,7 +680,7 @@ def _saved_input(x, x_scales, T, width, types):
     """(x_dtype, operand rows) of an input kept as it is (one of `types`) or as MXFP8 codes with their scales."""
     mx = x_scales is not None
     dt = DT_MXFP8 if mx else (DT.get(x.dtype, 0) if isinstance(x, torch.Tensor) else 0)
-    return dt, ((x, torch.uint8 if mx else types, "x", (T, width)), (x_scales, torch.uint8, "x_scales", (T, width // 32)))
+    return dt, ((x, torch.uint8 if mx else _one_of(x, types), "x", (T, width)), (x_scales, torch.uint8, "x_scales", (T, width // 32)))
 
 
 def moe_dense_linear_backward(dy, x, w, bias=None, act_fn="none", x_scales=None, want=("dx", "dw", "dbias"), out=None,
@@ -698,12 +701,11 @@ def moe_dense_linear_backward(dy, x, w, bias=None, act_fn="none", x_scales=None,
     _operands(dev, (dy, bf, "dy", None), *xitems, (w, bf, "w", (n, kdim)), (bias, torch.float32, "bias", (n,)),
               (ox, xt, "dx", (T, kdim)), (ow, bf, "dw", (n, kdim)), (ob, torch.float32, "dbias", (n,)))
     d, need = _dense_plan("linear_backward", T, n, kdim, _act_fn(act_fn), xdt, 0, DT[xt])
-    with _on(dy):
-        e = lambda o, on, shape, dt: None if not on else (o if o is not None else torch.empty(shape, dtype=dt, device=dev))
-        dx, dw, db = e(ox, fx, (T, kdim), xt), e(ow, fw, (n, kdim), bf), e(ob, fb, (n,), torch.float32)
-        ws, nws = _ws_for(ws, need, dev)
-        check(lib.moe_dense_linear_backward(ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(x_scales), _ptr(w), _ptr(bias),
-                                            _ptr(dx), _ptr(dw), _ptr(db), _ptr(ws), nws, _stream()))
+    e = lambda o, on, shape, dt: None if not on else (o if o is not None else torch.empty(shape, dtype=dt, device=dev))
+    dx, dw, db = e(ox, fx, (T, kdim), xt), e(ow, fw, (n, kdim), bf), e(ob, fb, (n,), torch.float32)
+    ws, nws = _ws_for(ws, need, dev)
+    _launch(dev, lib.moe_dense_linear_backward, d, _at(dy), _at(x), _at(x_scales), _at(w), _at(bias), _at(dx), _at(dw),
+            _at(db), _at(ws), nws)
     return dx, dw, db
 
 
@@ -723,13 +725,12 @@ def moe_dense_gateup(x, w_gate, w_up, b_gate=None, b_up=None, act_fn="silu", out
               (b_gate, torch.float32, "b_gate", (f,)), (b_up, torch.float32, "b_up", (f,)), (out, dt, "out", (T, f)),
               (pre, bf, "pre", (2, T, f)))
     d, need = _dense_plan("gateup", T, dm, f, _act_fn(act_fn), 0, DT[dt])
-    with _on(x):
-        h = out if out is not None else torch.empty((T, f), dtype=dt, device=dev)
-        if pre is None and want_pre:
-            pre = torch.empty((2, T, f), dtype=bf, device=dev)
-        ws, nws = _ws_for(ws, need, dev)
-        check(lib.moe_dense_gateup(ctypes.byref(d), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(b_gate), _ptr(b_up), _ptr(h),
-                                   _ptr(pre), _ptr(ws), nws, _stream()))
+    h = out if out is not None else torch.empty((T, f), dtype=dt, device=dev)
+    if pre is None and want_pre:
+        pre = torch.empty((2, T, f), dtype=bf, device=dev)
+    ws, nws = _ws_for(ws, need, dev)
+    _launch(dev, lib.moe_dense_gateup, d, _at(x), _at(w_gate), _at(w_up), _at(b_gate), _at(b_up), _at(h), _at(pre), _at(ws),
+            nws)
     return h, pre
 
 
@@ -743,7 +744,7 @@ def moe_dense_gateup_backward(dh, x, w_gate, w_up, b_gate=None, b_up=None, act_f
     T, f = _matrix(dh, "dh")
     dm = _matrix(w_gate, "w_gate")[1]
     fx, fw, fb = _wanted(want, ("dx", "dw", "db")) if want or not want_h else (False, False, False)
-    xdt, xitems = _saved_input(x, x_scales, T, dm, torch.bfloat16)
+    xdt, xitems = _saved_input(x, x_scales, T, dm, (torch.bfloat16,))
     dev = dh.device
     bf, f32 = torch.bfloat16, torch.float32
     o = out if out is not None else (None,) * 6
@@ -753,16 +754,15 @@ def moe_dense_gateup_backward(dh, x, w_gate, w_up, b_gate=None, b_up=None, act_f
     names = ("dx", "dw_gate", "dw_up", "db_gate", "db_up", "h")
     shapes = ((T, dm), (f, dm), (f, dm), (f,), (f,), (T, f))
     types = (bf, bf, bf, f32, f32, ht)
-    _operands(dev, (dh, tuple(DT), "dh", None), *xitems, (w_gate, bf, "w_gate", (f, dm)), (w_up, bf, "w_up", (f, dm)),
+    _operands(dev, (dh, _one_of(dh, DT), "dh", None), *xitems, (w_gate, bf, "w_gate", (f, dm)), (w_up, bf, "w_up", (f, dm)),
               (b_gate, f32, "b_gate", (f,)), (b_up, f32, "b_up", (f,)), (pre, bf, "pre", (2, T, f)),
               *((t, dt, nm, sh) for t, dt, nm, sh in zip(o, types, names, shapes)))
     d, need = _dense_plan("gateup_backward", T, dm, f, _act_fn(act_fn), xdt, DT[ht], DT[dh.dtype])
-    with _on(dh):
-        r = [None if not on else (t if t is not None else torch.empty(sh, dtype=dt, device=dev))
-             for t, dt, sh, on in zip(o, types, shapes, (fx, fw, fw, fb, fb, want_h))]
-        ws, nws = _ws_for(ws, need, dev)
-        check(lib.moe_dense_gateup_backward(ctypes.byref(d), _ptr(dh), _ptr(x), _ptr(x_scales), _ptr(w_gate), _ptr(w_up),
-                                            _ptr(b_gate), _ptr(b_up), _ptr(pre), *map(_ptr, r), _ptr(ws), nws, _stream()))
+    r = [None if not on else (t if t is not None else torch.empty(sh, dtype=dt, device=dev))
+         for t, dt, sh, on in zip(o, types, shapes, (fx, fw, fw, fb, fb, want_h))]
+    ws, nws = _ws_for(ws, need, dev)
+    _launch(dev, lib.moe_dense_gateup_backward, d, _at(dh), _at(x), _at(x_scales), _at(w_gate), _at(w_up), _at(b_gate),
+            _at(b_up), _at(pre), *map(_at, r), _at(ws), nws)
     return tuple(r)
 
 
@@ -772,13 +772,12 @@ def moe_mxfp8_quantize(x, out=None):
     rows, cols = _matrix(x, "x")
     dev = x.device
     codes, scales = out if out is not None else (None, None)
-    _operands(dev, (x, tuple(DT), "x", None), (codes, torch.uint8, "codes", (rows, cols)),
+    _operands(dev, (x, _one_of(x, DT), "x", None), (codes, torch.uint8, "codes", (rows, cols)),
               (scales, torch.uint8, "scales", (rows, cols // 32)))
-    with _on(x):
-        if out is None:
-            codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
-            scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
-        check(lib.moe_mxfp8_quantize(rows, cols, _ptr(x), DT[x.dtype], _ptr(codes), _ptr(scales), _stream()))
+    if out is None:
+        codes = torch.empty((rows, cols), dtype=torch.uint8, device=dev)
+        scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=dev)
+    _launch(dev, lib.moe_mxfp8_quantize, rows, cols, _at(x), DT[x.dtype], _at(codes), _at(scales))
     return codes, scales
 
 
@@ -791,7 +790,6 @@ def moe_mxfp8_dequant(codes, scales, out=None, out_dtype=torch.bfloat16):
         raise TypeError(f"values must be bfloat16 or float32 (got {dt})")
     _operands(dev, (codes, torch.uint8, "codes", None), (scales, torch.uint8, "scales", (rows, cols // 32)),
               (out, dt, "out", (rows, cols)))
-    with _on(codes):
-        o = out if out is not None else torch.empty((rows, cols), dtype=dt, device=dev)
-        check(lib.moe_mxfp8_dequant(rows, cols, _ptr(codes), _ptr(scales), _ptr(o), DT[dt], _stream()))
+    o = out if out is not None else torch.empty((rows, cols), dtype=dt, device=dev)
+    _launch(dev, lib.moe_mxfp8_dequant, rows, cols, _at(codes), _at(scales), _at(o), DT[dt])
     return o
