@@ -411,8 +411,9 @@ struct DenseProduct {
 // How a product runs.  The first `full` tiles (whole rounds of workgroups over the CUs, or all) run with
 // the epilogue in the product kernel; the sum of each of the rest is split into `split` parts over
 // workgroups of the same launch, whose float32 results a second kernel adds up, in order, and finishes.
+enum DenseTile { kTileL, kTileM, kTileS, kTileD, kTileW, kTiles };   // the shapes in dense_gemm.h
 struct DensePlan {
-    int cfg;              // tile shape: 0 L, 1 M, 2 S, 3 D (dense_gemm.h)
+    int cfg;              // kTile*
     int tr, tc;           // tiles along rows and columns
     int full, split;
     int steps;            // 64-value steps of the sum, all segments

@@ -8,18 +8,21 @@ namespace {
 constexpr int kCUs = 256;            // the plan is a pure function of the sizes (workspace queries run anywhere)
 
 // Tile shapes (dense_gemm.h) and their costs: us of a 64-value step of all the workgroups a CU holds, and
-// of a tile's start and end.  Fitted to 2400 timings of the four products over 16 to 4096 rows, 512 to
-// 7168 columns and sums of 32 to 7168 values, every shape and split forced in turn; the plan's choice is
-// within 2% of the fastest on average there.
+// of a tile's start and end.  Fitted to 2900 timings of the four products over 16 to 4096 rows, 1000 to
+// 7168 columns and sums of 32 to 7168 values, operands not in the caches, every shape and split forced in
+// turn; the plan's choice takes 1.5% longer than the fastest on average there, 16% at most.
 struct Tile {
     int br, bc, wr, per_cu;
     double step, tile;
 };
-constexpr Tile kTiles[4] = {
-    {256, 256, 2, 1, 1.01, 7.3}, {128, 128, 2, 2, 0.73, 4.1}, {64, 128, 1, 2, 0.39, 5.4}, {128, 128, 2, 1, 0.40, 4.2}};
-constexpr double kOnePerCu = 0.43;          // a step with one workgroup on a CU, relative to a full CU
+constexpr Tile kTileCosts[kTiles] = {{256, 256, 2, 1, 1.20, 8.0},
+                                     {128, 128, 2, 2, 1.02, 4.0},
+                                     {64, 128, 1, 2, 0.54, 5.8},
+                                     {128, 128, 2, 1, 0.46, 3.75},
+                                     {128, 128, 2, 4, 1.75, 7.4}};
+constexpr double kOnePerCu = 0.41;          // a step with one workgroup on a CU, relative to a full CU
 constexpr int kMaxSplit = 8;
-constexpr double kPartBytesPerUs = 8.5e6;   // partial results written and read back (they stay in the caches)
+constexpr double kPartBytesPerUs = 6.8e6;   // partial results written and read back (partly in the caches)
 constexpr double kFinishUs = 5.0;           // the launch that sums them
 
 }  // namespace
@@ -32,9 +35,10 @@ DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg, int ter
     double best_t = 1e30;
     const int steps = (K + 63) / 64 * nseg;
     const int mats = pair ? 2 : 1;
-    for (int cfg = 0; cfg < 4; ++cfg) {
-        if (form == kFormTN && cfg == 2) continue;
-        const Tile &t = kTiles[cfg];
+    for (int cfg = 0; cfg < kTiles; ++cfg) {
+        // S cannot hold a strided rows operand; D's extra step in flight does not pay over the tokens' sums, which W takes
+        if (form == kFormTN ? cfg == kTileS || cfg == kTileD : cfg == kTileW) continue;
+        const Tile &t = kTileCosts[cfg];
         const int tr = (R + t.br - 1) / t.br, tc = (C + t.bc / mats - 1) / (t.bc / mats);
         const int64_t tiles = (int64_t)tr * tc, slots = (int64_t)kCUs * t.per_cu;
         // rounds of n workgroups of s steps each; a last round with fewer workgroups per CU runs faster

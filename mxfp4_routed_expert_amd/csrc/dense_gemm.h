@@ -34,6 +34,10 @@ struct CfgS {                // 4 waves of 64 x 32, two workgroups a CU
     static constexpr int BR = 64, BC = 128, WR = 1, WC = 4, kStages = 3;
     static constexpr bool kAlternate = false;
 };
+struct CfgW {                // as M with one buffer and one set of operands: four workgroups a CU, for the short sums of weight gradients
+    static constexpr int BR = 128, BC = 128, WR = 2, WC = 2, kStages = 1;
+    static constexpr bool kAlternate = false;
+};
 struct CfgD {                // as M with a step more in flight, one workgroup a CU
     static constexpr int BR = 128, BC = 128, WR = 2, WC = 2, kStages = 3;
     static constexpr bool kAlternate = false;
@@ -92,7 +96,7 @@ struct Operand {
 };
 
 template <class Cfg, int FORM, class Epi>
-__global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, 2) void dense_gemm_kernel(const GemmArgs ga, Epi epi) {
+__global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, Cfg::kStages == 1 ? 4 : 2) void dense_gemm_kernel(const GemmArgs ga, Epi epi) {
     constexpr int BR = Cfg::BR, BC = Cfg::BC, NW = Cfg::WR * Cfg::WC;
     constexpr int TR = BR / Cfg::WR / 16, TC = BC / Cfg::WC / 16;
     constexpr bool RS = FORM == kFormTN, CS = FORM != kFormNT, PAIR = Epi::kPair;
@@ -388,6 +392,19 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, 2) void dense_gemm_kernel(co
             if (wave >= NW / 2) run(std::true_type{});
             else run(std::false_type{});
         }
+    } else if constexpr (Cfg::kStages == 1) {
+        // the CU's other workgroups multiply while this one copies
+        Frags f;
+        for (int s = s0; s < s1; ++s) {
+            issue(0);
+            asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+            for (int ks = 0; ks < kBK / 32; ++ks) {
+                read(f, 0, ks);
+                multiply(f);
+            }
+            if (s + 1 < s1) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        }
     } else {
         // Operands are read one 32-value half step ahead of the products that use them, so reads and matrix
         // instructions overlap.  After the barrier in the middle of step s every operand of it has been read:
@@ -445,11 +462,12 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, 2) void dense_gemm_kernel(co
     }
 
     // ---- epilogue.  Lane (lr, lg) of MFMA tile (i, j) holds columns 4 lg .. 4 lg + 3 of row lr.  The
-    // wave's tile goes through LDS (64 rows at a time, 16-byte chunk c of row r at c ^ (r & 15 or 7)) so
+    // wave's tile goes through LDS (32 or 64 rows at a time, 16-byte chunk c of row r at c ^ (r & 15 or 7)) so
     // that 8 or 16 neighbouring lanes take one row: whole lines are read and written, and the
     // epilogue's code appears once.
     constexpr int kCh = 4 * TC;                              // 16-byte chunks of a float32 row of the wave's tile
-    constexpr int kJP = TR < 4 ? TR : 4;                     // MFMA tile rows per pass
+    // MFMA tile rows per pass: as many as the operands' LDS holds, at most 4
+    constexpr int kJP = NW * 4 * 16 * kCh * 16 <= Cfg::kStages * kStage ? 4 : 2;
     constexpr int kLanes = PAIR ? kCh / 2 : kCh, kRows = 64 / kLanes;
     constexpr int U = 4;                                     // row groups handled together
     static_assert(NW * kJP * 16 * kCh * 16 <= Cfg::kStages * kStage, "the passes fit in the operands' LDS");
@@ -533,10 +551,13 @@ moe_status dense_run_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &
 
 template <int FORM, class Epi>
 moe_status dense_run(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s) {
-    if (pl.cfg == 0) return dense_run_cfg<CfgL, FORM>(p, pl, e, part, s);
-    if (pl.cfg == 3) return dense_run_cfg<CfgD, FORM>(p, pl, e, part, s);
-    if constexpr (FORM != kFormTN)
-        if (pl.cfg == 2) return dense_run_cfg<CfgS, FORM>(p, pl, e, part, s);
+    if (pl.cfg == kTileL) return dense_run_cfg<CfgL, FORM>(p, pl, e, part, s);
+    if constexpr (FORM == kFormTN) {
+        if (pl.cfg == kTileW) return dense_run_cfg<CfgW, FORM>(p, pl, e, part, s);
+    } else {
+        if (pl.cfg == kTileS) return dense_run_cfg<CfgS, FORM>(p, pl, e, part, s);
+        if (pl.cfg == kTileD) return dense_run_cfg<CfgD, FORM>(p, pl, e, part, s);
+    }
     return dense_run_cfg<CfgM, FORM>(p, pl, e, part, s);
 }
 
