@@ -442,8 +442,6 @@ moe_status dense_linear_bwd_product(const DenseProduct &p, const DensePlan &pl, 
                                     hipStream_t s);
 moe_status dense_gate_bwd_product(const DenseProduct &p, const DensePlan &pl, const EpiGateBwd &e, float *part,
                                   hipStream_t s);
-moe_status dense_nn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, hipStream_t s);
-moe_status dense_tn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, hipStream_t s);
 
 // Sum the parts of the split tiles and run the epilogue on the sums (dense_aux.hip).  br x bc: the tile.
 // Partial results: [split tile][part][br][bc], a pair tile's columns gate first.
@@ -453,11 +451,69 @@ moe_status dense_finish(const DenseProduct &p, const DensePlan &pl, int br, int 
 constexpr int kFinishRows = 16;   // rows per workgroup there, and per column-sum row of the launch
 constexpr int kSavedRows = 2;     // rows per workgroup of the saved pre-activations' gradients
 
-// out[c] = sum over rows of part[row][c] (column-sum partials), in row order.
-moe_status dense_colsum_reduce(const float *part, int rows, int ld, int C0, float *out0, float *out1, hipStream_t s);
-// Column-sum partials of a bf16 matrix [R][C]: part [ceil(R / kColRows)][csld].
-constexpr int kColRows = 64;
-moe_status dense_colsum(const uint16_t *a, int R, int C, float *part, int csld, hipStream_t s);
+// Column sums, in two steps of a fixed order: partial sums of kColRows rows of a bf16 matrix [rows][C]
+// (kSideSum: out0 [ceil(rows / kColRows)][ld]), and the sum of partial rows [rows][ld] (kSideReduce: columns
+// below C to out0, the next C to out1 unless it is NULL).  Either runs as its own launch or as further
+// workgroups of a gradient product's.
+constexpr int kColRows = 32;
+enum DenseSideKind { kSideNone, kSideSum, kSideReduce };
+struct DenseSide {
+    int kind, rows, C, ld;
+    const void *in;
+    float *out0, *out1;
+};
+// workgroups of `threads` threads that a job takes
+inline int dense_side_wgs(const DenseSide &j, int threads) {
+    if (j.kind == kSideSum) return (j.rows + kColRows - 1) / kColRows * ((j.C + 4 * threads - 1) / (4 * threads));
+    if (j.kind == kSideReduce) return ((j.out1 ? 2 : 1) * j.C + 63) / 64;
+    return 0;
+}
+// workgroup `wg` of a job; lds: 64 floats a wave
+template <int THREADS>
+MOE_DEV void dense_side_job(const DenseSide &j, int wg, float *lds) {
+    if (j.kind == kSideSum) {
+        const int n = (j.C + 4 * THREADS - 1) / (4 * THREADS);
+        const int rb = wg / n, c = (wg - rb * n) * 4 * THREADS + 4 * threadIdx.x;
+        if (c >= j.C) return;
+        const uint16_t *a = (const uint16_t *)j.in;
+        const int r0 = rb * kColRows, r1 = min(j.rows, r0 + kColRows);
+        f32x4 s = {0.f, 0.f, 0.f, 0.f};
+        if ((j.C & 3) == 0) {
+#pragma unroll 8
+            for (int r = r0; r < r1; ++r) s += load4_bf16(a + (size_t)r * j.C + c);
+        } else {
+            for (int r = r0; r < r1; ++r)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (c + q < j.C) s[q] += bf16_to_f32(a[(size_t)r * j.C + c + q]);
+        }
+        *(f32x4 *)(j.out0 + (size_t)rb * j.ld + c) = s;
+        return;
+    }
+    // 64 columns a workgroup; each wave sums its share of the rows, the waves' sums are joined in order
+    constexpr int W = THREADS / 64;
+    const int lane = lane_id(), w = wave_id();
+    const int C = (j.out1 ? 2 : 1) * j.C, c = wg * 64 + lane;
+    const int lo = (int)((int64_t)j.rows * w / W), hi = (int)((int64_t)j.rows * (w + 1) / W);
+    const float *part = (const float *)j.in;
+    float s = 0.0f;
+    if (c < C) {
+#pragma unroll 8
+        for (int r = lo; r < hi; ++r) s += part[(size_t)r * j.ld + c];
+    }
+    lds[w * 64 + lane] = s;
+    __syncthreads();
+    if (w == 0 && c < C) {
+        for (int i = 1; i < W; ++i) s += lds[i * 64 + lane];
+        if (c < j.C) j.out0[c] = s;
+        else j.out1[c - j.C] = s;
+    }
+}
+moe_status dense_side_launch(const DenseSide &j, hipStream_t s);
+moe_status dense_nn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, const DenseSide &side,
+                            hipStream_t s);
+moe_status dense_tn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, const DenseSide &side,
+                            hipStream_t s);
 // Gradients of the gated product from saved pre-activations [2][R][C] (dense_aux.hip).
 moe_status dense_gate_bwd_saved(const EpiGateBwd &e, const uint16_t *pre, int R, hipStream_t s);
 // float32 rows [n] -> three bf16 planes [3][n] whose sum is the value exactly.

@@ -10,20 +10,31 @@ constexpr int kCUs = 256;            // the plan is a pure function of the sizes
 // Tile shapes (dense_gemm.h) and their costs: us of a 64-value step of all the workgroups a CU holds, and
 // of a tile's start and end.  Fitted to 2900 timings of the four products over 16 to 4096 rows, 1000 to
 // 7168 columns and sums of 32 to 7168 values, operands not in the caches, every shape and split forced in
-// turn; the plan's choice takes 1.5% longer than the fastest on average there, 16% at most.
+// turn; there the plan's choice takes 0.5% longer than the fastest on average (weight gradients 2.3%) and
+// 15% at most.  A weight gradient's sum is short and its result large, hence costs of its own.
 struct Tile {
     int br, bc, wr, per_cu;
     double step, tile;
 };
-constexpr Tile kTileCosts[kTiles] = {{256, 256, 2, 1, 1.20, 8.0},
-                                     {128, 128, 2, 2, 1.02, 4.0},
-                                     {64, 128, 1, 2, 0.54, 5.8},
-                                     {128, 128, 2, 1, 0.46, 3.75},
-                                     {128, 128, 2, 4, 1.75, 7.4}};
-constexpr double kOnePerCu = 0.41;          // a step with one workgroup on a CU, relative to a full CU
+struct TileCosts {
+    Tile t[kTiles];
+    double one;                             // a step with one workgroup on a CU, relative to a full CU
+    double finish;                          // us of the launch that sums partial results
+    double part;                            // their bytes written or read in a us (partly in the caches)
+};
+constexpr TileCosts kCosts = {{{256, 256, 2, 1, 1.41, 4.7},
+                               {128, 128, 2, 2, 1.05, 4.9},
+                               {64, 128, 1, 2, 0.57, 6.2},
+                               {128, 128, 2, 1, 0.53, 4.3},
+                               {128, 128, 2, 4, 0.0, 0.0}},
+                              0.43, 4.9, 9.0e6};
+constexpr TileCosts kWeightGradCosts = {{{256, 256, 2, 1, 1.26, 5.7},
+                                         {128, 128, 2, 2, 0.91, 3.0},
+                                         {64, 128, 1, 2, 0.0, 0.0},
+                                         {128, 128, 2, 1, 0.0, 0.0},
+                                         {128, 128, 2, 4, 1.65, 5.2}},
+                                        0.30, 2.0, 6.7e6};
 constexpr int kMaxSplit = 8;
-constexpr double kPartBytesPerUs = 6.8e6;   // partial results written and read back (partly in the caches)
-constexpr double kFinishUs = 5.0;           // the launch that sums them
 
 }  // namespace
 
@@ -35,17 +46,18 @@ DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg, int ter
     double best_t = 1e30;
     const int steps = (K + 63) / 64 * nseg;
     const int mats = pair ? 2 : 1;
+    const TileCosts &costs = form == kFormTN ? kWeightGradCosts : kCosts;
     for (int cfg = 0; cfg < kTiles; ++cfg) {
         // S cannot hold a strided rows operand; D's extra step in flight does not pay over the tokens' sums, which W takes
         if (form == kFormTN ? cfg == kTileS || cfg == kTileD : cfg == kTileW) continue;
-        const Tile &t = kTileCosts[cfg];
+        const Tile &t = costs.t[cfg];
         const int tr = (R + t.br - 1) / t.br, tc = (C + t.bc / mats - 1) / (t.bc / mats);
         const int64_t tiles = (int64_t)tr * tc, slots = (int64_t)kCUs * t.per_cu;
         // rounds of n workgroups of s steps each; a last round with fewer workgroups per CU runs faster
         auto rounds = [&](int64_t n, int s) {
             if (n <= 0) return 0.0;
             const int64_t k = (n + slots - 1) / slots, last = (n - (k - 1) * slots + kCUs - 1) / kCUs;
-            const double share = t.per_cu == 1 ? 1.0 : kOnePerCu + (1.0 - kOnePerCu) * (double)last / t.per_cu;
+            const double share = t.per_cu == 1 ? 1.0 : costs.one + (1.0 - costs.one) * (double)last / t.per_cu;
             return ((double)(k - 1) + share) * (s * t.step + t.tile);
         };
         for (int split = 1; split <= kMaxSplit; ++split) {
@@ -56,7 +68,7 @@ DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg, int ter
             const size_t bytes = (size_t)tail * split * t.br * t.bc * sizeof(float);
             if (tail > 0) {
                 const double live = (double)(R < t.br ? R : t.br) / t.br;
-                us += kFinishUs + bytes * live * 2.0 / kPartBytesPerUs;
+                us += costs.finish + bytes * live * 2.0 / costs.part;
             }
             if (us < best_t) {
                 best_t = us;
@@ -80,6 +92,18 @@ struct Carve {
         at = align_up(at + bytes, 256);
         return (T *)q;
     }
+};
+
+// Jobs that run in order beside the products of a call: those that no product is left for run at once.
+struct Sides {
+    DenseSide job[2] = {};
+    int n = 0, at = 0;
+    void add(const DenseSide &j) { job[n++] = j; }
+    moe_status keep(int products, hipStream_t s) {
+        for (; n - at > products; ++at) MOE_TRY(dense_side_launch(job[at], s));
+        return MOE_OK;
+    }
+    DenseSide next() { return at < n ? job[at++] : DenseSide{}; }
 };
 
 bool fn_ok(int fn) { return fn >= MOE_FN_NONE && fn <= MOE_FN_RELU; }
@@ -350,13 +374,16 @@ extern "C" moe_status moe_dense_linear_backward(const moe_linear_desc *d, const 
         MOE_TRY(dense_linear_bwd_product(p, b.pz, e, b.part, s));
         dz = b.dz;
     } else if (T > 0) {
-        if (dbias) MOE_TRY(dense_colsum(dz, T, n, b.cs, b.csld, s));
         if (b.own_dz && (dx || dw)) {
             MOE_TRY(dense_pad_rows(dz, b.dz, T, n, b.ldz, s));
             dz = b.dz;
         }
     }
-    if (dbias) MOE_TRY(dense_colsum_reduce(b.cs, T > 0 ? b.cs_rows : 0, b.csld, n, dbias, nullptr, s));
+    // the bias gradient's column sums ride along with the products: the sums of dy where dz is dy, then their total
+    Sides sides;
+    if (dbias && !act && T > 0) sides.add(DenseSide{kSideSum, T, n, b.csld, dy, b.cs, nullptr});
+    if (dbias) sides.add(DenseSide{kSideReduce, T > 0 ? b.cs_rows : 0, n, b.csld, b.cs, dbias, nullptr});
+    MOE_TRY(sides.keep((dx && T > 0) + (dw != nullptr), s));
     if (dx && T > 0) {
         DenseProduct p = {};
         p.nseg = 1;
@@ -374,7 +401,7 @@ extern "C" moe_status moe_dense_linear_backward(const moe_linear_desc *d, const 
         e.rows0 = T;
         e.C = k;
         e.f32 = d->dx_dtype == MOE_DT_F32;
-        MOE_TRY(dense_nn_product(p, b.px, e, b.part, s));
+        MOE_TRY(dense_nn_product(p, b.px, e, b.part, sides.next(), s));
     }
     if (dw) {
         // dz's leading term with x's one or two leading terms, then dz's low term with x's first
@@ -398,7 +425,7 @@ extern "C" moe_status moe_dense_linear_backward(const moe_linear_desc *d, const 
         e.rows0 = n;
         e.C = k;
         e.f32 = 0;
-        MOE_TRY(dense_tn_product(p, b.pw, e, b.part, s));
+        MOE_TRY(dense_tn_product(p, b.pw, e, b.part, sides.next(), s));
     }
     return MOE_OK;
 }
@@ -498,8 +525,10 @@ extern "C" moe_status moe_dense_gateup_backward(const moe_gateup_desc *d, const 
             MOE_TRY(dense_gate_bwd_product(p, b.pg, e, b.part, s));
         }
     }
+    Sides sides;
     if (db_gate)
-        MOE_TRY(dense_colsum_reduce(b.cs, T == 0 ? 0 : (pre ? b.cs_rows_saved : b.cs_rows), 2 * f, f, db_gate, db_up, s));
+        sides.add(DenseSide{kSideReduce, T == 0 ? 0 : (pre ? b.cs_rows_saved : b.cs_rows), f, 2 * f, b.cs, db_gate, db_up});
+    MOE_TRY(sides.keep((dx && T > 0) + (dw_gate != nullptr), s));
     if (dx && T > 0) {
         DenseProduct p = {};
         p.nseg = 2;
@@ -519,7 +548,7 @@ extern "C" moe_status moe_dense_gateup_backward(const moe_gateup_desc *d, const 
         e.rows0 = T;
         e.C = dm;
         e.f32 = 0;
-        MOE_TRY(dense_nn_product(p, b.px, e, b.part, s));
+        MOE_TRY(dense_nn_product(p, b.px, e, b.part, sides.next(), s));
     }
     if (dw_gate) {
         DenseProduct p = {};
@@ -541,7 +570,7 @@ extern "C" moe_status moe_dense_gateup_backward(const moe_gateup_desc *d, const 
         e.rows0 = f;
         e.C = dm;
         e.f32 = 0;
-        MOE_TRY(dense_tn_product(p, b.pw, e, b.part, s));
+        MOE_TRY(dense_tn_product(p, b.pw, e, b.part, sides.next(), s));
     }
     return MOE_OK;
 }

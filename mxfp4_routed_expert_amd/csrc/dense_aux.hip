@@ -100,46 +100,9 @@ __global__ __launch_bounds__(kThreads) void gate_bwd_saved_kernel(const uint16_t
     }
 }
 
-// Column sums of kColRows rows of a bf16 matrix.
-__global__ __launch_bounds__(kThreads) void colsum_kernel(const uint16_t *__restrict__ a, int R, int C,
-                                                          float *__restrict__ part, int ld) {
-    const Block bl = block_of(C);
-    const int c = bl.cb * kCols + threadIdx.x * 4;
-    if (c >= C) return;
-    const int r0 = bl.rb * kColRows, r1 = min(R, r0 + kColRows);
-    f32x4 s = {0.f, 0.f, 0.f, 0.f};
-    if ((C & 3) == 0) {
-#pragma unroll 8
-        for (int r = r0; r < r1; ++r) s += load4_bf16(a + (size_t)r * C + c);
-    } else {
-        for (int r = r0; r < r1; ++r)
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (c + q < C) s[q] += bf16_to_f32(a[(size_t)r * C + c + q]);
-    }
-    *(f32x4 *)(part + (size_t)bl.rb * ld + c) = s;
-}
-
-// Sum the partial rows: 64 columns a workgroup, four quarters of the rows, joined in order.
-__global__ __launch_bounds__(kThreads) void colsum_reduce_kernel(const float *__restrict__ part, int rows, int ld, int C0,
-                                                                 float *__restrict__ out0, float *__restrict__ out1) {
-    __shared__ float s_q[4][64];
-    const int lane = lane_id(), q = wave_id();
-    const int C = out1 ? 2 * C0 : C0;
-    const int c = blockIdx.x * 64 + lane;
-    const int lo = (int)((int64_t)rows * q / 4), hi = (int)((int64_t)rows * (q + 1) / 4);
-    float s = 0.0f;
-    if (c < C) {
-#pragma unroll 8
-        for (int r = lo; r < hi; ++r) s += part[(size_t)r * ld + c];
-    }
-    s_q[q][lane] = s;
-    __syncthreads();
-    if (q == 0 && c < C) {
-        const float v = ((s_q[0][lane] + s_q[1][lane]) + s_q[2][lane]) + s_q[3][lane];
-        if (c < C0) out0[c] = v;
-        else out1[c - C0] = v;
-    }
+__global__ __launch_bounds__(kThreads) void side_kernel(const DenseSide j) {
+    __shared__ float s_sum[kThreads];
+    dense_side_job<kThreads>(j, blockIdx.x, s_sum);
 }
 
 // v = hi + mid + lo exactly, each term the top eight significant bits of what is left
@@ -220,15 +183,10 @@ moe_status dense_gate_bwd_saved(const EpiGateBwd &e, const uint16_t *pre, int R,
     return launch_check("gated gradients");
 }
 
-moe_status dense_colsum(const uint16_t *a, int R, int C, float *part, int csld, hipStream_t s) {
-    hipLaunchKernelGGL(colsum_kernel, block_grid(R, kColRows, C), dim3(kThreads), 0, s, a, R, C, part, csld);
-    return launch_check("column sums");
-}
-
-moe_status dense_colsum_reduce(const float *part, int rows, int ld, int C0, float *out0, float *out1, hipStream_t s) {
-    const int C = out1 ? 2 * C0 : C0;
-    hipLaunchKernelGGL(colsum_reduce_kernel, dim3((unsigned)((C + 63) / 64)), dim3(kThreads), 0, s, part, rows, ld, C0, out0,
-                       out1);
+moe_status dense_side_launch(const DenseSide &j, hipStream_t s) {
+    const int wgs = dense_side_wgs(j, kThreads);
+    if (wgs == 0) return MOE_OK;
+    hipLaunchKernelGGL(side_kernel, dim3((unsigned)wgs), dim3(kThreads), 0, s, j);
     return launch_check("column sums");
 }
 

@@ -51,6 +51,8 @@ struct GemmArgs {
     int tr, tc, full, split, steps, seg_steps;
     int cs_sub;           // column-sum rows per wave row of a tile
     float *part;
+    int main_wgs;         // workgroups of the product; those past them run `side`
+    DenseSide side;
 };
 
 __device__ __attribute__((aligned(16))) const uint32_t g_dense_zero[4] = {0, 0, 0, 0};
@@ -106,6 +108,11 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, Cfg::kStages == 1 ? 4 : 2) v
     constexpr int kStage = OpR::kBytes + OpC::kBytes;
     extern __shared__ __align__(16) unsigned char smem[];
 
+    if constexpr (std::is_same_v<Epi, EpiStore>)
+        if ((int)blockIdx.x >= ga.main_wgs) {
+            dense_side_job<64 * NW>(ga.side, blockIdx.x - ga.main_wgs, (float *)smem);
+            return;
+        }
     const DenseProduct &p = ga.p;
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
     const int wr = wave / Cfg::WC, wc = wave % Cfg::WC;
@@ -537,28 +544,29 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, Cfg::kStages == 1 ? 4 : 2) v
 
 // The product with its epilogue, and the sum of its split tiles.
 template <class Cfg, int FORM, class Epi>
-moe_status dense_run_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s) {
+moe_status dense_run_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, const DenseSide &side, hipStream_t s) {
     constexpr int lds = Cfg::kStages * (Cfg::BR + Cfg::BC) * kBK * 2;
     const int tiles = pl.tr * pl.tc;
     const bool tail = pl.full < tiles;
     GemmArgs ga{p, pl.tr, pl.tc, pl.full, pl.split, pl.steps, (p.K + kBK - 1) / kBK, tail ? Cfg::BR / Cfg::WR / kFinishRows : 1,
-                part};
-    hipLaunchKernelGGL((dense_gemm_kernel<Cfg, FORM, Epi>), dim3((unsigned)(pl.full + (tiles - pl.full) * pl.split)),
+                part, pl.full + (tiles - pl.full) * pl.split, side};
+    hipLaunchKernelGGL((dense_gemm_kernel<Cfg, FORM, Epi>), dim3((unsigned)(ga.main_wgs + dense_side_wgs(side, 64 * Cfg::WR * Cfg::WC))),
                        dim3(64 * Cfg::WR * Cfg::WC), lds, s, ga, e);
     MOE_TRY(launch_check("dense product"));
     return tail ? dense_finish(p, pl, Cfg::BR, Cfg::BC, e, part, s) : MOE_OK;
 }
 
 template <int FORM, class Epi>
-moe_status dense_run(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s) {
-    if (pl.cfg == kTileL) return dense_run_cfg<CfgL, FORM>(p, pl, e, part, s);
+moe_status dense_run(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s,
+                     const DenseSide &side = {}) {
+    if (pl.cfg == kTileL) return dense_run_cfg<CfgL, FORM>(p, pl, e, part, side, s);
     if constexpr (FORM == kFormTN) {
-        if (pl.cfg == kTileW) return dense_run_cfg<CfgW, FORM>(p, pl, e, part, s);
+        if (pl.cfg == kTileW) return dense_run_cfg<CfgW, FORM>(p, pl, e, part, side, s);
     } else {
-        if (pl.cfg == kTileS) return dense_run_cfg<CfgS, FORM>(p, pl, e, part, s);
-        if (pl.cfg == kTileD) return dense_run_cfg<CfgD, FORM>(p, pl, e, part, s);
+        if (pl.cfg == kTileS) return dense_run_cfg<CfgS, FORM>(p, pl, e, part, side, s);
+        if (pl.cfg == kTileD) return dense_run_cfg<CfgD, FORM>(p, pl, e, part, side, s);
     }
-    return dense_run_cfg<CfgM, FORM>(p, pl, e, part, s);
+    return dense_run_cfg<CfgM, FORM>(p, pl, e, part, side, s);
 }
 
 }  // namespace moe

@@ -4,11 +4,13 @@
 
 namespace moe {
 
-moe_status dense_nn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, hipStream_t s) {
-    return dense_run<kFormNN>(p, pl, e, part, s);
+moe_status dense_nn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, const DenseSide &side,
+                            hipStream_t s) {
+    return dense_run<kFormNN>(p, pl, e, part, s, side);
 }
-moe_status dense_tn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, hipStream_t s) {
-    return dense_run<kFormTN>(p, pl, e, part, s);
+moe_status dense_tn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, const DenseSide &side,
+                            hipStream_t s) {
+    return dense_run<kFormTN>(p, pl, e, part, s, side);
 }
 
 }  // namespace moe
