@@ -1,7 +1,8 @@
 // Dense products of a few tokens (T <= 8): one pass over the weights on the vector ALU.
 //
-// Bound by the weight bytes.  A workgroup of four waves owns four consecutive output columns
-// (four gate and four up rows for the pair); its waves take every fourth 512-value piece of the
+// Bound by the weight bytes (one token, 2048 x 7168: 6.4 us, 4.6 TB/s; gate and up of 2368 x 7168: 13.5 us,
+// 5.0 TB/s).  A workgroup of four waves owns four consecutive output columns (four gate and four up rows
+// for the pair, eight columns with several float32 rows); its waves take every fourth 512-value piece of the
 // sum, a lane 8 consecutive values of each row, so every load is a whole 1 KiB line run of one
 // row and a wave keeps 8 or more of them in flight.  The tokens' values of a piece are read once
 // per wave from the L2 and used for all the rows.  bf16 rows multiply with v_dot2_f32_bf16,
@@ -37,22 +38,23 @@ MOE_DEV void butterfly(float (&v)[V]) {
     for (; o > 0; o >>= 1) v[0] += __shfl_xor(v[0], o, kWave);
 }
 
-template <int MT, bool F32X, class Epi>
+template <int MT, bool F32X, int G, class Epi>
 __global__ __launch_bounds__(64 * kWaves) void dense_gemv_kernel(const void *__restrict__ x, const uint16_t *__restrict__ w0,
                                                                  const uint16_t *__restrict__ w1, int T, int n, int K,
                                                                  Epi epi) {
-    constexpr int NM = Epi::kPair ? 2 : 1, ROWS = 4 * NM, V = ROWS * MT;
+    constexpr int NM = Epi::kPair ? 2 : 1, ROWS = 4 * NM * G, V = ROWS * MT;
+    static_assert(NM == 1 || G == 1, "a pair is two groups of rows");
     static_assert(V <= 64, "one value per lane after the butterfly");
     __shared__ float s_sum[kWaves][V];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
-    const int c = blockIdx.x * 4;
+    const int c = blockIdx.x * (4 * G);
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
 
     const uint16_t *wrow[ROWS];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) wrow[i] = (i < 4 ? w0 : w1) + (size_t)min(c + (i & 3), n - 1) * K;
+    for (int i = 0; i < ROWS; ++i) wrow[i] = (NM == 2 && i >= 4 ? w1 : w0) + (size_t)min(c + (NM == 2 ? i & 3 : i), n - 1) * K;
 
     // 8 values of every row and token from value k on; past the end of the sum both are zero
     auto piece = [&](int k, bool live) {
@@ -109,27 +111,38 @@ __global__ __launch_bounds__(64 * kWaves) void dense_gemv_kernel(const void *__r
     constexpr int kLanesPer = 64 / V;
     if (lane % kLanesPer == 0) s_sum[wave][lane / kLanesPer] = acc[0];
     __syncthreads();
-    const int t = threadIdx.x;
-    if (t < T) {
+    const int t = threadIdx.x % MT, g = threadIdx.x / MT;    // token and group of four columns
+    if (g < G && t < T && c + 4 * g < n) {
         f32x4 a[1] = {kZero4}, b[1] = {kZero4}, ca, cb;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int w = 0; w < kWaves; ++w) {
-                a[0][q] += s_sum[w][q * MT + t];
+                a[0][q] += s_sum[w][(4 * g + q) * MT + t];
                 if constexpr (NM == 2) b[0][q] += s_sum[w][(4 + q) * MT + t];
             }
-        epi.rows(epi.cols(c), t, 1, T, c, a, b, ca, cb);
+        epi.rows(epi.cols(c + 4 * g), t, 1, T, c + 4 * g, a, b, ca, cb);
     }
 }
 
+// G groups of four columns a workgroup: with four or more float32 rows their own bytes, read by every
+// workgroup, outweigh four weight rows', so eight are taken (T = 4, 7168 x 2048: 10.5 -> 10.0 us; T = 8,
+// 7168 x 2368: 19.3 -> 17.0 us); otherwise the smaller workgroups fill the CUs better (T = 1,
+// 2048 x 7168: 6.9 us against 7.5).
 template <bool F32X, class Epi>
 moe_status launch(const void *x, const uint16_t *w0, const uint16_t *w1, int T, int n, int K, const Epi &e, hipStream_t s) {
-    const dim3 grid((unsigned)((n + 3) / 4)), block(64 * kWaves);
-    if (T == 1) hipLaunchKernelGGL((dense_gemv_kernel<1, F32X, Epi>), grid, block, 0, s, x, w0, w1, T, n, K, e);
-    else if (T == 2) hipLaunchKernelGGL((dense_gemv_kernel<2, F32X, Epi>), grid, block, 0, s, x, w0, w1, T, n, K, e);
-    else if (T <= 4) hipLaunchKernelGGL((dense_gemv_kernel<4, F32X, Epi>), grid, block, 0, s, x, w0, w1, T, n, K, e);
-    else hipLaunchKernelGGL((dense_gemv_kernel<8, F32X, Epi>), grid, block, 0, s, x, w0, w1, T, n, K, e);
+    constexpr int G = F32X ? 2 : 1;
+    auto run = [&](auto mt, auto g) {
+        constexpr int MT = decltype(mt)::value, GG = decltype(g)::value;
+        hipLaunchKernelGGL((dense_gemv_kernel<MT, F32X, GG, Epi>), dim3((unsigned)((n + 4 * GG - 1) / (4 * GG))),
+                           dim3(64 * kWaves), 0, s, x, w0, w1, T, n, K, e);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Many = std::integral_constant<int, G>;
+    if (T == 1) run(One{}, One{});
+    else if (T == 2) run(std::integral_constant<int, 2>{}, One{});
+    else if (T <= 4) run(std::integral_constant<int, 4>{}, Many{});
+    else run(std::integral_constant<int, 8>{}, Many{});
     return launch_check("dense product of a few tokens");
 }
 
