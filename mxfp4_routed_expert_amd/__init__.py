@@ -5,7 +5,7 @@ exposes each entry point with the same name, `layer` composes one layer step and
 feed-forward block with its training step.
 """
 from . import binding  # noqa: F401  (raises ImportError when the library is not built)
-from .binding import (ExpertWeights, MoeError, decode_step_sync, moe_combine, moe_dense_bf16, moe_dequant, moe_dequant_bf16,  # noqa: F401
+from .binding import (DenseWeights, ExpertWeights, MoeError, decode_step_sync, moe_combine, moe_dense_bf16, moe_dequant, moe_dequant_bf16,  # noqa: F401
                       moe_decode_step, moe_expert_down, moe_expert_down_combine, moe_expert_ffn, moe_expert_gateup,
                       moe_dense_gateup, moe_dense_gateup_backward, moe_dense_linear, moe_dense_linear_backward,
                       moe_expert_gateup_shared, moe_mx_quantize, moe_mxfp8_dequant, moe_mxfp8_quantize, moe_permute, moe_route, moe_route_permute,

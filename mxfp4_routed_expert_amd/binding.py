@@ -306,6 +306,22 @@ class ExpertWeights:
                              t(es.down), t(es.down_s))
 
 
+@dataclass
+class DenseWeights:
+    """Device tensors of one expert with bf16 weights: gate, up [d_ff][d_model], down [d_model][d_ff]."""
+    gate: torch.Tensor
+    up: torch.Tensor
+    down: torch.Tensor
+
+    @property
+    def d_model(self):
+        return self.gate.shape[1]
+
+    @property
+    def d_ff(self):
+        return self.gate.shape[0]
+
+
 def moe_expert_ffn(w: ExpertWeights, x, act="float", k=1, expert_offsets=None, sorted_pairs=None, out=None,
                    ws=None):
     """y_rows [R][d_model] float32; R = T*k (routed) or T (expert_offsets None, one expert)."""

@@ -3,7 +3,8 @@
 route -> permute -> routed experts (moe_expert_ffn) -> shared expert (moe_expert_ffn,
 identity form) -> combine; LatentMoE layers add moe_dense_bf16 before the routed experts
 and after the combine (Kimi K3 article, architecture section); a gated shared expert's
-output is scaled by its gate before it is added after the up projection.  Decode-sized
+output is scaled by its gate before it is added after the up projection.  A shared expert
+with bf16 weights (DenseWeights) runs as moe_dense_gateup and moe_dense_linear.  Decode-sized
 LatentMoE steps run the routed down product and the combine into z as one down-combine
 launch.  Decode-sized
 batches use the fused calls instead, three kernels a step -- the router's logits; the
@@ -34,7 +35,7 @@ class LayerWeights:
     experts: B.ExpertWeights
     logit_bias: torch.Tensor | None = None
     select_bias: torch.Tensor | None = None
-    shared: B.ExpertWeights | None = None
+    shared: B.ExpertWeights | B.DenseWeights | None = None   # DenseWeights: a bf16 shared expert
     w_shared_gate: torch.Tensor | None = None  # bf16 [H]
     p_down: torch.Tensor | None = None     # bf16 [L][H]
     p_up: torch.Tensor | None = None       # bf16 [H][L]
@@ -63,10 +64,10 @@ def down_combine_lds(k: int, shared: bool, d_ff: int) -> int:
 def fuses(w: LayerWeights, T: int) -> bool:
     """Whether a step of T tokens takes the fused decode calls: decode-sized batches
     (T <= 4) with FLOAT activations and no latent projections, a shared expert (if any)
-    of the routed format and widths, and k + 1 rows of d_ff within the LDS limit."""
+    of the routed format and widths (a bf16 one runs as its own calls), and k + 1 rows of d_ff within the LDS limit."""
     ex, sh = w.experts, w.shared
     return (w.act == "float" and w.p_down is None and w.p_up is None and 1 <= T <= 4
-            and (sh is None or (sh.fmt == ex.fmt and sh.d_model == ex.d_model and sh.d_ff == ex.d_ff))
+            and (sh is None or (isinstance(sh, B.ExpertWeights) and sh.fmt == ex.fmt and sh.d_model == ex.d_model and sh.d_ff == ex.d_ff))
             and down_combine_lds(w.k, sh is not None, ex.d_ff) <= FUSED_LDS_LIMIT)
 
 
@@ -117,12 +118,17 @@ class MoELayer:
         self.hq = e(T * k, I // 2, dt=torch.uint8) if mx else None
         self.hs = e(T * k, I // 32, dt=torch.uint8) if mx else None
         self.ws_gu = B._workspace(B.moe_expert_gateup_workspace(w.experts, w.act, T, k), device)
-        staged_sh = sh is not None and not self.fused
+        # a bf16 shared expert: dense products from x itself, h in float32 as the routed experts'
+        self.dense_sh = isinstance(sh, B.DenseWeights)
+        staged_sh = sh is not None and not self.fused and not self.dense_sh
         Is = sh.d_ff if sh is not None else 0
         self.h_sh = e(T, Is) if sh is not None else None
         self.hq_sh = e(T, Is // 2, dt=torch.uint8) if (staged_sh and mx) else None
         self.hs_sh = e(T, Is // 32, dt=torch.uint8) if (staged_sh and mx) else None
         self.ws_gu_sh = B._workspace(B.moe_expert_gateup_workspace(sh, w.act, T, 1), device) if staged_sh else None
+        if self.dense_sh:
+            need = max(B.moe_dense_gateup_workspace(T, H, Is, "silu", f32), B.moe_dense_linear_workspace(T, H, Is, x_dtype=f32, out_dtype=f32))
+            self.ws_gu_sh = B._workspace(need, device)
         # otherwise the shared expert does not depend on routing: it runs on a second stream,
         # joined before the combine, so it overlaps router, permutation and routed experts;
         # so does the latent down-projection, which the routed gate/up waits for
@@ -180,7 +186,10 @@ class MoELayer:
                 if w.p_down is not None:
                     xe = B.moe_dense_bf16(x, w.p_down, out=self.x_lat)
                     self.lat_ready.record(self.side)
-                if w.shared is not None:
+                if self.dense_sh:
+                    B.moe_dense_gateup(x, w.shared.gate, w.shared.up, out=self.h_sh, ws=self.ws_gu_sh)
+                    B.moe_dense_linear(self.h_sh, w.shared.down, out=self.y_s, ws=self.ws_gu_sh)
+                elif w.shared is not None:
                     B.moe_expert_gateup(w.shared, x, w.act, 1, None, None,
                                         out=(None if mx else self.h_sh, self.hq_sh, self.hs_sh), ws=self.ws_gu_sh)
                     B.moe_expert_down(w.shared, self.T, w.act, 1, None, self.h_sh, self.hq_sh, self.hs_sh,

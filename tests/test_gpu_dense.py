@@ -417,3 +417,51 @@ def test_binding_refusals(M):
         with pytest.raises(exc):
             call()
             pytest.fail(f"call {i} was not refused")
+
+
+@pytest.mark.parametrize("T", [1, 3, 40, 130])
+@pytest.mark.parametrize("gated", [False, True])
+def test_layer_with_bf16_shared_expert(M, T, gated):
+    import dataclasses
+
+    import numpy as np
+
+    import gpu_common as G
+    import synth
+    from oracle import layer as OL
+    cfg = dataclasses.replace(synth.get("tiny"), T=T)
+    dev = torch.device("cuda:0")
+    t, inp = G.build(cfg, dev)
+    w = G.layer_weights(cfg, t)
+    f = 136
+    w.shared = M.DenseWeights(rnd(1, f, cfg.H, std=0.06), rnd(2, f, cfg.H, std=0.06), rnd(3, cfg.H, f, std=0.08))
+    w.w_shared_gate = rnd(4, cfg.H, std=0.05) if gated else None
+    layer = M.MoELayer(w, T, dev)
+    assert not layer.fused
+    out = layer.forward(t["x"])
+    x = t["x"].double()
+    g, u = x @ w.shared.gate.double().t(), x @ w.shared.up.double().t()
+    y = (R.act("silu", g)[0] * u) @ w.shared.down.double().t()
+    if gated:
+        y = y * torch.sigmoid(x @ w.w_shared_gate.double())[:, None]
+    ge, _ = G.host_expert_getter(cfg)
+    routed = OL.layer(cfg, inp, ge, None)
+    G.assert_close(G.to_np(out), routed.out + y.cpu().numpy(), f"layer T={T} gated={gated}")
+    out = out.clone()
+    # the same step in a graph, replayed over other tokens between eager steps
+    x2 = torch.empty_like(t["x"])
+    x2.copy_(t["x"])
+    layer.forward(x2)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = layer.forward(x2)
+    eager = M.MoELayer(w, T, dev)
+    for it in range(3):
+        x2.copy_(rnd(60 + it, T, cfg.H) if it else t["x"])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, eager.forward(x2))
+        if it == 0:
+            assert torch.equal(o, out)
+        torch.cuda.synchronize()
