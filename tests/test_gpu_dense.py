@@ -288,6 +288,80 @@ def test_no_tokens(M):
     assert M.moe_mxfp8_quantize(x)[0].shape == (0, 64)
 
 
+# (rows, columns, sum) at which the forward and input-gradient products take each tile shape (256 x 256, 128 x 128 in
+# its two forms, 64 x 128) with the sum whole, split for the tiles of a last partial round, and split everywhere
+TILES = [(9, 264, 136), (260, 7176, 136), (260, 7176, 328), (1030, 7176, 136), (9, 264, 1160), (70, 2056, 2376), (130, 7176, 4104),
+         (4100, 264, 7176), (520, 7176, 2376), (1030, 4104, 2376), (2060, 7176, 1160), (1100, 7176, 2376)]
+# the gated products' (tokens, d_ff, d_model)
+PAIR_TILES = [(9, 264, 136), (130, 7176, 136), (130, 7176, 328), (520, 7176, 136), (9, 264, 1160), (70, 1032, 2376), (130, 4104, 4104),
+              (700, 1032, 7176), (260, 7176, 2376), (1030, 2056, 2376), (2060, 7176, 520), (4100, 1032, 4104)]
+# input gradients of the gated products (tokens, d_model, d_ff): a sum of two parts
+TWO_PART_TILES = [(70, 264, 136), (260, 7176, 136), (1030, 7176, 136), (70, 264, 520), (70, 2056, 1160), (130, 7176, 2376),
+                  (520, 7176, 1160), (1030, 4104, 1160), (4100, 4104, 328)]
+# weight gradients (tokens, n, k)
+GRAD_TILES = [(9, 1032, 7176), (70, 4104, 7176), (520, 264, 136), (1030, 1032, 7176), (5200, 264, 7176), (5200, 2376, 1160),
+              (1030, 4104, 4104), (2600, 4104, 4104)]
+
+
+def rnd_gpu(seed, *shape, std=1.0, dtype=bf16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+@pytest.mark.parametrize("T,n,k", TILES)
+def test_linear_tiles(M, T, n, k):
+    n -= 3                                   # rows of odd length
+    x, w, b, r = rnd_gpu(1, T, k), rnd_gpu(2, n, k, std=k ** -0.5), rnd_gpu(3, n, dtype=f32), rnd_gpu(4, T, n)
+    R.check(M.moe_dense_linear(x, w, b, "gelu", r), R.linear(x, w, b, "gelu", r, bf16), "y")
+    x = x.float() + rnd_gpu(5, T, k, std=2 ** -12, dtype=f32)
+    R.check(M.moe_dense_linear(x, w, None, "none"), R.linear(x, w, None, "none", None, f32), "y of float32 rows")
+
+
+def _linear_backward(M, T, n, k, fn):
+    x, w, b, dy = rnd_gpu(1, T, k), rnd_gpu(2, n, k, std=k ** -0.5), rnd_gpu(3, n, dtype=f32), rnd_gpu(4, T, n)
+    got = M.moe_dense_linear_backward(dy, x, w, b, fn)
+    for name, g, r in zip(("dx", "dw", "dbias"), got, R.linear_backward(dy, x, w, b, fn)):
+        R.check(g, r, name)
+
+
+@pytest.mark.parametrize("T,n,k", TILES)
+def test_linear_backward_tiles(M, T, n, k):
+    _linear_backward(M, T, n, k, "silu")
+
+
+@pytest.mark.parametrize("T,k,n", TILES[1:])
+def test_input_gradient_tiles(M, T, k, n):
+    _linear_backward(M, T, n - 1, k, "none")  # an odd n: dz is dy with padded rows
+
+
+@pytest.mark.parametrize("T,n,k", GRAD_TILES)
+def test_weight_gradient_tiles(M, T, n, k):
+    _linear_backward(M, T, n, k, "none")
+
+
+def _gateup(M, T, d, f, bias):
+    x, wg, wu = rnd_gpu(1, T, d), rnd_gpu(2, f, d, std=d ** -0.5), rnd_gpu(3, f, d, std=d ** -0.5)
+    bg, bu = (rnd_gpu(4, f, dtype=f32), rnd_gpu(5, f, dtype=f32)) if bias else (None, None)
+    dh = rnd_gpu(6, T, f)
+    h, pre = M.moe_dense_gateup(x, wg, wu, bg, bu, "gelu_tanh", want_pre=True)
+    R.check(h, R.gateup(x, wg, wu, bg, bu, "gelu_tanh", bf16), "h")
+    for p in (None, pre):
+        got = M.moe_dense_gateup_backward(dh, x, wg, wu, bg, bu, "gelu_tanh", pre=p, want_h=True)
+        ref = R.gateup_backward(dh, x, wg, wu, bg, bu, "gelu_tanh", p)
+        for name, g, r in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up", "h"), got, ref):
+            R.check(g, r, name)
+
+
+@pytest.mark.parametrize("T,f,d", PAIR_TILES)
+def test_gateup_tiles(M, T, f, d):
+    _gateup(M, T, d, f, True)
+
+
+@pytest.mark.parametrize("T,d,f", TWO_PART_TILES)
+def test_gateup_input_gradient_tiles(M, T, d, f):
+    _gateup(M, T, d, f, False)
+
+
 def _block_ref(x, xb, wg, wu, wd, res, dy):
     """float64 block and gradients; h is rounded to bf16 between the products beyond 64 tokens, its gradient never."""
     T = x.shape[0]
