@@ -35,14 +35,14 @@ MOE_DEV uint16_t bf16_bits(float v) { return (uint16_t)(pack2_bf16(v, 0.0f) & 0x
 //   gelu_tanh  0.5 z (1 + tanh q) = z s(2q), q = sqrt(2/pi) (z + 0.044715 z^3): the logistic form
 //              has no cancellation for negative z         f' = s + z s (1 - s) 2q'
 //   relu       max(z, 0) (NaN stays NaN)                 f' = [z > 0]
-// 1 - s is taken as e s with e = exp(-t), so it keeps its relative accuracy where s rounds to 1.
+// 1 - s is taken as e s with e = exp(-t), so it keeps its relative accuracy where s rounds to 1; there
+// e is held below infinity (as is z^2 in q'), so that a product with a zero stays zero for every finite z.
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluA = 1.5957691216057308f;           // 2 sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
 MOE_DEV float gelu_arg(float z) { return z * (kGeluA + (kGeluA * kGeluB) * z * z); }
-// exp(-t), held below infinity so that its product with a zero stays zero
-MOE_DEV float exp_neg(float t) { return fminf(__builtin_amdgcn_exp2f(-kLog2e * t), 1e38f); }
+MOE_DEV float exp_neg(float t) { return __builtin_amdgcn_exp2f(-kLog2e * t); }
 MOE_DEV float rcp(float v) { return __builtin_amdgcn_rcpf(v); }
 
 // erfc(x) / 2 for x = |z| / sqrt 2, given E = exp(-z^2 / 2): E times a polynomial in t = 1 / (1 + 0.4 x)
@@ -95,7 +95,7 @@ MOE_DEV void act_grad_rows(int fn, f32x4 (&z)[U], f32x4 (&d)[U]) {
     auto logistic = [](float &v, float t, float dt, float &g) {
         const float e = exp_neg(t), s = rcp(1.0f + e);
         v *= s;
-        g = s + v * (e * s * dt);
+        g = s + v * (fminf(e, 1e38f) * s * dt);
     };
     if (fn == MOE_FN_SILU) {
         each([&](float &v, float &g) { logistic(v, v, 1.0f, g); });
@@ -106,7 +106,7 @@ MOE_DEV void act_grad_rows(int fn, f32x4 (&z)[U], f32x4 (&d)[U]) {
             g = p + z * (0.39894228040143268f * E);
         });
     } else if (fn == MOE_FN_GELU_TANH) {
-        each([&](float &v, float &g) { logistic(v, gelu_arg(v), kGeluA + (3.0f * kGeluA * kGeluB) * v * v, g); });
+        each([&](float &v, float &g) { logistic(v, gelu_arg(v), kGeluA + (3.0f * kGeluA * kGeluB) * fminf(v * v, 1e30f), g); });
     } else if (fn == MOE_FN_RELU) {
         each([](float &v, float &g) {
             g = v > 0.0f ? 1.0f : 0.0f;

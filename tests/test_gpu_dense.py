@@ -106,6 +106,30 @@ def test_nonfinite_values_stay_in_their_rows(M, T):
     assert torch.isnan(y[2]).all() and not torch.isfinite(y[:, 70].float()).all()
 
 
+@pytest.mark.parametrize("T", [2, 12, 80])
+@pytest.mark.parametrize("fn", FNS[1:])
+def test_activations_of_huge_arguments(M, fn, T):
+    # f is z or 0 and f' 1 or 0 for every finite argument this far out, also where its powers overflow
+    v = torch.tensor([s * m for m in (1e3, 1e5, 1e13, 1e20, 3e38) for s in (1, -1)] + [0.0] * 6).to(bf16).cuda()
+    x = torch.zeros(T, 8, dtype=bf16, device="cuda")
+    x[:, 0] = 1
+    w = torch.zeros(16, 8, dtype=bf16, device="cuda")
+    w[:, 0] = v
+    one = torch.ones(T, 16, dtype=bf16, device="cuda")
+    f, on = v.float().clamp(min=0).expand(T, 16), (v[:10] > 0).float()
+    assert torch.equal(M.moe_dense_linear(x, w, None, fn, out_dtype=f32), f)
+    _, dw, db = M.moe_dense_linear_backward(one, x, w, None, fn, want=("dw", "dbias"))
+    assert torch.equal(db[:10], T * on) and torch.equal(dw[:10, 0].float(), T * on)
+    wu = torch.zeros_like(w)
+    wu[:, 0] = 1
+    h, pre = M.moe_dense_gateup(x, w, wu, act_fn=fn, out_dtype=f32, want_pre=True)
+    assert torch.equal(h, f)
+    for p in (None, pre):
+        got = M.moe_dense_gateup_backward(one, x, w, wu, act_fn=fn, pre=p, want=("dw", "db"), want_h=True, h_dtype=f32)
+        assert torch.equal(got[3][:10], T * on) and torch.equal(got[1][:10, 0].float(), T * on)
+        assert torch.equal(got[5], f) and (got[4][v <= 0] == 0).all()
+
+
 GATE = [(1, 8, 8), (1, 2048, 200), (2, 72, 40), (4, 520, 136), (7, 512, 64), (9, 136, 8), (33, 64, 264), (64, 264, 72),
         (100, 200, 136), (257, 72, 520), (520, 520, 328), (1100, 264, 2368)]
 
