@@ -139,7 +139,11 @@ moe_status check_linear(const char *who, const moe_linear_desc *d, bool backward
         MOE_REQUIRE(d->x_dtype == MOE_DT_BF16 || d->x_dtype == MOE_DT_F32, "%s: unknown x_dtype %d", who, d->x_dtype);
         MOE_REQUIRE(d->y_dtype == MOE_DT_BF16 || d->y_dtype == MOE_DT_F32, "%s: unknown y_dtype %d", who, d->y_dtype);
     }
-    MOE_REQUIRE(fits31(d->T, (int64_t)d->n + 8) && fits31(d->n, d->kdim) && fits31(d->T, d->kdim), "%s: sizes overflow int32", who);
+    // (the terms of few rows form one operand, whose tile offsets are 32-bit bytes: three of x, two of dz)
+    const int64_t x_rows = (int64_t)d->T * (d->T <= kTermTokens && d->x_dtype == MOE_DT_F32 ? 3 : 1);
+    const int64_t z_rows = (int64_t)d->T * (d->T <= kTermTokens && backward ? 2 : 1);
+    MOE_REQUIRE(fits31(z_rows, (int64_t)d->n + 8) && fits31(d->n, d->kdim) && fits31(x_rows, d->kdim), "%s: sizes overflow int32",
+                who);
     return MOE_OK;
 }
 
@@ -223,7 +227,8 @@ moe_status check_gateup(const char *who, const moe_gateup_desc *d, bool backward
         MOE_REQUIRE(d->x_dtype == MOE_DT_BF16, "%s: x must be bf16 (x_dtype %d)", who, d->x_dtype);
     }
     MOE_REQUIRE(d->h_dtype == MOE_DT_BF16 || d->h_dtype == MOE_DT_F32, "%s: unknown h_dtype %d", who, d->h_dtype);
-    MOE_REQUIRE(fits31(d->T, 2 * (int64_t)d->d_ff) && fits31(d->d_model, 2 * (int64_t)d->d_ff) &&
+    const int64_t g_rows = (int64_t)d->T * (d->T <= kTermTokens && backward ? 2 : 1);     // (terms of dg and du)
+    MOE_REQUIRE(fits31(g_rows, 2 * (int64_t)d->d_ff) && fits31(d->d_model, 2 * (int64_t)d->d_ff) &&
                     fits31(d->T, d->d_model),
                 "%s: sizes overflow int32", who);
     return MOE_OK;

@@ -127,6 +127,21 @@ def test_mxfp8_refusals():
     assert lib.moe_mxfp8_quantize(0, 64, None, 0, None, None, None) == B.MOE_OK
 
 
+@pytest.mark.parametrize("T", [16, 64])
+def test_kept_terms_count_in_the_size_limit(T):
+    # up to 64 tokens dz, dg and du are kept as two terms and a float32 x as three, in one operand each
+    fits, over = (2 ** 31 - 1) // (2 * T) - 15, 2 ** 31 // (2 * T)
+    n = fits - fits % 8
+    assert lib.moe_dense_linear_backward_workspace(lin(T=T, n=n, kdim=8, fn=1)) > 0
+    refused(lib.moe_dense_linear_backward(lin(T=T, n=over, kdim=8, fn=1), P, P, None, P, None, P, P, P, P, BIG, None),
+            B.MOE_ERR_INVALID_ARG, "overflow")
+    k = 2 ** 31 // (3 * T) // 8 * 8 + 8
+    refused(lib.moe_dense_linear(lin(T=T, n=1, kdim=k, x_dtype=1), P, P, None, None, P, P, BIG, None), B.MOE_ERR_INVALID_ARG, "overflow")
+    f = 2 ** 31 // (4 * T)
+    refused(lib.moe_dense_gateup_backward(gate(T=T, d_model=8, d_ff=f), P, P, None, P, P, None, None, None, P, P, P, P, P, P, P, BIG, None),
+            B.MOE_ERR_INVALID_ARG, "overflow")
+
+
 def test_workspaces_do_not_depend_on_a_gpu():
     # a pure function of the sizes: the same on every query, and finite for the largest call
     d = dict(T=4096, d_model=7168, d_ff=2368)
