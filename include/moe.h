@@ -404,7 +404,7 @@ moe_status moe_mx_quantize(int32_t rows, int32_t cols, const void *x, int32_t x_
  *   may be NULL (not wanted), not all.  The residual's gradient is dy.
  *   x may be NULL when fn is MOE_FN_NONE and dw is NULL; w when fn is MOE_FN_NONE and dx is NULL.
  *   bias is read only when fn is not MOE_FN_NONE.  y_dtype is ignored.
- *   With T == 0 dw and dbias are written as zeros.
+ *   With T == 0 dw and dbias are written as zeros, and nothing need be asked for.
  */
 typedef struct {
     int32_t T, n, kdim;
@@ -438,7 +438,7 @@ size_t moe_dense_linear_backward_workspace(const moe_linear_desc *desc);
  *   gradient.  For dx and dw_*, dg and du are rounded to bf16 when T > 64 and kept as two bf16 terms
  *   up to there; the bias gradients sum the unrounded values.  dw_gate and dw_up come together or
  *   not at all, as do db_gate and db_up; dx, dw_*, db_* and h may be NULL, not all.
- *   With T == 0 the weight and bias gradients are written as zeros.
+ *   With T == 0 the weight and bias gradients are written as zeros, and nothing need be asked for.
  */
 typedef struct {
     int32_t T, d_model, d_ff;

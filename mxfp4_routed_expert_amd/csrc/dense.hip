@@ -333,7 +333,7 @@ extern "C" moe_status moe_dense_linear_backward(const moe_linear_desc *d, const 
                                                 void *dw, float *dbias, void *ws, size_t ws_bytes, moe_stream stream) {
     clear_error();
     MOE_TRY(check_linear("moe_dense_linear_backward", d, true));
-    MOE_REQUIRE(dx || dw || dbias, "moe_dense_linear_backward: no gradient asked for");
+    MOE_REQUIRE(dx || dw || dbias || d->T == 0, "moe_dense_linear_backward: no gradient asked for");
     const bool act = d->fn != MOE_FN_NONE, mx = d->x_dtype == MOE_DT_MXFP8;
     const bool need_x = act || dw, need_w = act || dx;
     if (d->T > 0) {
@@ -485,7 +485,7 @@ extern "C" moe_status moe_dense_gateup_backward(const moe_gateup_desc *d, const 
     MOE_TRY(check_gateup("moe_dense_gateup_backward", d, true));
     MOE_REQUIRE(!dw_gate == !dw_up && !db_gate == !db_up,
                 "moe_dense_gateup_backward: the gate's and up's gradients come together");
-    MOE_REQUIRE(dx || dw_gate || db_gate || h, "moe_dense_gateup_backward: no result asked for");
+    MOE_REQUIRE(dx || dw_gate || db_gate || h || d->T == 0, "moe_dense_gateup_backward: no result asked for");
     const bool mx = d->x_dtype == MOE_DT_MXFP8, need_x = !pre || dw_gate;
     if (d->T > 0) {
         MOE_REQUIRE(dh && w_gate && w_up && (x || !need_x), "moe_dense_gateup_backward: NULL dh, x, w_gate or w_up");

@@ -127,6 +127,14 @@ def test_mxfp8_refusals():
     assert lib.moe_mxfp8_quantize(0, 64, None, 0, None, None, None) == B.MOE_OK
 
 
+def test_no_tokens_and_nothing_to_write():
+    # an empty dx has no address: with no tokens that is no refusal
+    e = (None,) * 3
+    assert lib.moe_dense_linear_backward(lin(T=0, fn=1), None, None, None, None, None, None, None, None, P, BIG, None) == B.MOE_OK
+    assert lib.moe_dense_gateup_backward(gate(T=0), None, None, None, None, None, None, None, None, *e, None, None, None, P, BIG,
+                                         None) == B.MOE_OK
+
+
 @pytest.mark.parametrize("T", [16, 64])
 def test_kept_terms_count_in_the_size_limit(T):
     # up to 64 tokens dz, dg and du are kept as two terms and a float32 x as three, in one operand each

@@ -312,6 +312,15 @@ def test_no_tokens(M):
     assert M.moe_mxfp8_quantize(x)[0].shape == (0, 64)
 
 
+@pytest.mark.parametrize("checkpoint", ["bf16", "mxfp8"])
+def test_block_of_no_tokens(M, checkpoint):
+    ffn = M.DenseFFN(rnd(1, 40, 64), rnd(2, 40, 64), rnd(3, 64, 40), 0, checkpoint=checkpoint)
+    x = torch.empty(0, 64, dtype=bf16, device="cuda")
+    assert ffn.forward(x, x, train=True).shape == (0, 64)
+    dx, *dws = ffn.backward(x)
+    assert dx.shape == (0, 64) and all((g == 0).all() for g in dws)
+
+
 # (rows, columns, sum) at which the forward and input-gradient products take each tile shape (256 x 256, 128 x 128 in
 # its two forms, 64 x 128) with the sum whole, split for the tiles of a last partial round, and split everywhere
 TILES = [(9, 264, 136), (260, 7176, 136), (260, 7176, 328), (1030, 7176, 136), (9, 264, 1160), (70, 2056, 2376), (130, 7176, 4104),
