@@ -586,6 +586,8 @@ def moe_mx_quantize(x):
 def _operands(dev, *items):
     """items: (tensor or None, dtype or tuple of dtypes, name, shape or None).  Each on `dev`, of its dtype and shape,
     contiguous.  (One expression a tensor when all is well: a decoded token's call is a few microseconds.)"""
+    if dev.type != "cuda":
+        raise ValueError(f"{items[0][2]} must live in device memory (got {dev})")
     for t, dtype, name, shape in items:
         if t is None or (isinstance(t, torch.Tensor) and (t.dtype is dtype) and t.device == dev and t.is_contiguous()
                          and (shape is None or t.shape == shape)):

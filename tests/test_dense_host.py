@@ -193,3 +193,13 @@ def test_mxfp8_definition_against_float8():
     lim = torch.maximum(lim, (x.double().abs() - 448 * torch.exp2(scales.double() - 127).repeat_interleave(32, 1)))
     assert (err <= lim).all()
     assert math.isnan(R.mxfp8_values(torch.zeros(1, 32, dtype=torch.uint8), torch.tensor([[255]], dtype=torch.uint8))[0, 0])
+
+
+def test_binding_refuses_host_tensors():
+    x, w, c = torch.zeros(4, 64).bfloat16(), torch.zeros(32, 64).bfloat16(), torch.zeros(4, 64, dtype=torch.uint8)
+    h = torch.zeros(4, 32).bfloat16()
+    for call in (lambda: B.moe_dense_linear(x, w), lambda: B.moe_dense_linear_backward(h, x, w), lambda: B.moe_dense_gateup(x, w, w),
+                 lambda: B.moe_dense_gateup_backward(h, x, w, w), lambda: B.moe_mxfp8_quantize(x),
+                 lambda: B.moe_mxfp8_dequant(c, c[:, :2].contiguous())):
+        with pytest.raises(ValueError, match="device memory"):
+            call()
