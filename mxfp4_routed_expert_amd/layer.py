@@ -67,7 +67,8 @@ def fuses(w: LayerWeights, T: int) -> bool:
     of the routed format and widths (a bf16 one runs as its own calls), and k + 1 rows of d_ff within the LDS limit."""
     ex, sh = w.experts, w.shared
     return (w.act == "float" and w.p_down is None and w.p_up is None and 1 <= T <= 4
-            and (sh is None or (isinstance(sh, B.ExpertWeights) and sh.fmt == ex.fmt and sh.d_model == ex.d_model and sh.d_ff == ex.d_ff))
+            and (sh is None or (not isinstance(sh, B.DenseWeights) and sh.fmt == ex.fmt and sh.d_model == ex.d_model
+                                and sh.d_ff == ex.d_ff))
             and down_combine_lds(w.k, sh is not None, ex.d_ff) <= FUSED_LDS_LIMIT)
 
 
