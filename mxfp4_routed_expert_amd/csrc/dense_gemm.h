@@ -259,20 +259,24 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, Cfg::kStages == 1 ? 4 : 2) v
     struct Frags {
         bf16x8 r[TR], c[TC];
     };
-    auto read = [&](Frags &f, int st, int ks) MOE_INLINE {
-        const int base_r = st * kStage, base_c = st * kStage + OpR::kBytes;
-#pragma unroll
-        for (int j = 0; j < TR; ++j) {
+    // operand q of a half step, in the order the products want them: a column operand, the row operands, the other
+    // column operands
+    auto read_one = [&](Frags &f, auto qq, int st, int ks) MOE_INLINE {
+        constexpr int q = decltype(qq)::value;
+        if constexpr (q >= 1 && q <= TR) {
+            constexpr int j = q - 1;
             const int f0 = wr * 16 * TR + 16 * j;
-            if constexpr (RS) f.r[j] = frag_s(base_r, f0, ks, std::integral_constant<int, BR>{});
-            else f.r[j] = frag_c(base_r, f0, ks);
+            if constexpr (RS) f.r[j] = frag_s(st * kStage, f0, ks, std::integral_constant<int, BR>{});
+            else f.r[j] = frag_c(st * kStage, f0, ks);
+        } else {
+            constexpr int i = q == 0 ? 0 : q - TR;
+            const int f0 = wc * 16 * TC + 16 * i, base = st * kStage + OpR::kBytes;
+            if constexpr (CS) f.c[i] = frag_s(base, f0, ks, std::integral_constant<int, BC>{});
+            else f.c[i] = frag_c(base, f0, ks);
         }
-#pragma unroll
-        for (int i = 0; i < TC; ++i) {
-            const int f0 = wc * 16 * TC + 16 * i;
-            if constexpr (CS) f.c[i] = frag_s(base_c, f0, ks, std::integral_constant<int, BC>{});
-            else f.c[i] = frag_c(base_c, f0, ks);
-        }
+    };
+    auto read = [&](Frags &f, int st, int ks) MOE_INLINE {
+        static_for<TR + TC>([&](auto q) MOE_INLINE { read_one(f, q, st, ks); });
     };
     // The products of one half step, with the whole copies P0 .. P1-1 into stage st spread between them: a copy
     // occupies the CU's address unit for 16 cycles, and a wave that issues one after another waits for it
@@ -291,6 +295,26 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, Cfg::kStages == 1 ? 4 : 2) v
                 __builtin_amdgcn_sched_barrier(0);
             }
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.c[i], f.r[j], acc[i][j], 0, 0, 0);
+        });
+    };
+    // The products of one half step with the reads of the next one's operands between them (a wave that issues its
+    // reads one after another waits for the LDS instead of multiplying), and the whole copies P0 .. P1-1 into stage cst.
+    auto multiply_read = [&](const Frags &f, Frags &g, int st, int ks, auto p0, auto p1, int cst) MOE_INLINE {
+        constexpr int NM = TC * TR, NR = TR + TC, read_every = NM * 3 / 4 / NR > 1 ? NM * 3 / 4 / NR : 1;
+        constexpr int n = decltype(p1)::value - decltype(p0)::value, every = NM / (n > 0 ? n : 1);
+        static_assert((n == 0 || every >= 1) && NR * read_every <= NM + read_every - 1, "reads and copies between products");
+        static_for<NM>([&](auto m) MOE_INLINE {
+            constexpr int i = m / TR, j = m % TR;
+            if constexpr (m % read_every == 0 && m / read_every < NR) {
+                read_one(g, std::integral_constant<int, m / read_every>{}, st, ks);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f.c[i], f.r[j], acc[i][j], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+            if constexpr (n > 0 && m % every == every - 1 && m / every < n) {
+                piece(std::integral_constant<int, decltype(p0)::value + m / every>{}, cst, std::false_type{});
+                __builtin_amdgcn_sched_barrier(0);
+            }
         });
     };
     auto multiply = [&](const Frags &f) MOE_INLINE { multiply_copy(f, Zero{}, Zero{}, 0); };
@@ -444,17 +468,9 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, Cfg::kStages == 1 ? 4 : 2) v
                 st = st + 1 == kStages ? 0 : st + 1;
                 if (!COPY && s + kStages < s1) issue(free);
                 reads_done();
-                read(f0, st, 0);
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (COPY) multiply_copy(f1, Zero{}, Half{}, free);
-                else multiply(f1);
-                __builtin_amdgcn_sched_barrier(0);
+                multiply_read(f1, f0, st, 0, Zero{}, std::conditional_t<COPY, Half, Zero>{}, free);
                 reads_done();
-                read(f1, st, 1);
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (COPY) multiply_copy(f0, Half{}, All{}, free);
-                else multiply(f0);
-                __builtin_amdgcn_sched_barrier(0);
+                multiply_read(f0, f1, st, 1, Half{}, std::conditional_t<COPY, All, Half>{}, free);
                 if constexpr (COPY) next_source();
             };
             int s = s0;
