@@ -411,7 +411,7 @@ struct DenseProduct {
 // How a product runs.  The first `full` tiles (whole rounds of workgroups over the CUs, or all) run with
 // the epilogue in the product kernel; the sum of each of the rest is split into `split` parts over
 // workgroups of the same launch, whose float32 results a second kernel adds up, in order, and finishes.
-enum DenseTile { kTileL, kTileM, kTileS, kTileD, kTileW, kTiles };   // the shapes in dense_gemm.h
+enum DenseTile { kTileL, kTileM, kTileS, kTileD, kTileW, kTileB, kTiles };   // the shapes in dense_gemm.h
 struct DensePlan {
     int cfg;              // kTile*
     int tr, tc;           // tiles along rows and columns

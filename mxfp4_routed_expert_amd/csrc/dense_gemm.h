@@ -3,8 +3,8 @@
 // A workgroup computes one BR x BC tile of the output; each wave owns a (16 TR) x (16 TC) part as
 // MFMA tiles.  The columns operand is the MFMA's first operand and the rows operand its second,
 // so a lane's four accumulators are four consecutive columns of one row.  The sum advances in
-// steps of 64 values, both operands of a step in LDS, two steps resident: step s+1 is copied
-// global -> LDS (no registers) while step s is multiplied; one barrier a step.
+// steps of 64 values; the operands of one to three steps (kStages) are in LDS, copied there from
+// global memory without passing through registers, while earlier ones are multiplied.
 //
 // LDS of a step.  An operand contiguous along the sum is kept as rows of 64 values (128 bytes),
 // 16-byte chunk c of row r at position c ^ ((r >> 1) & 7): an operand read takes one chunk of 16
@@ -13,15 +13,26 @@
 // transposing LDS read (ds_read_b64_tr_b16): a group of 16 lanes supplies 4 rows of 16 values and
 // lane i receives column i of the four.  Its 16-byte chunk c of row k sits at c ^ 2g(k), g(k) =
 // (k & 3) | ((k >> 3) & 1) << 2: the eight 32-byte row pieces that half a wave reads then fall on
-// eight different bank groups.
+// eight different bank groups.  (The conflict counter reads 0 for all three forms.)
 //
 // Values past the end of the sum are copied from a zero page (for both operands), rows past the
 // end of a matrix repeat its last row and their results are not stored.
+//
+// What bounds it.  A step of the 256 x 256 tile takes 0.85 us of matrix instructions per CU and as much of
+// LDS bandwidth; it measures 1.05 - 1.15 us with its operands in the last-level cache (4096 x 4096 x 8192:
+// 182 us, 1.51 PFLOP/s) and 1.3 - 1.4 from HBM.  A step of a 128 x 128 tile measures 0.41 us from the
+// last-level cache and 0.58 from HBM: a CU's misses in flight are limited, to 47 bytes a ns from HBM and 77
+// from the last-level cache against 115 of L2 hits, however many copies are issued ahead (four and five
+// stages measured the same as three).
 #pragma once
 #include "dense.h"
 
 namespace moe {
 
+// The shapes, with sizes at which each is the fastest (us, operands from HBM).  4093 x 7168 x 2048: L 115, B 128, M
+// 148, D 157, S 163; 1024 x 7168 x 2048: B 34.5, M 40, D 46, S 52, L 56; 512 x 7168 x 2368: D 28, S 34, B 36,
+// M 39, L 63; input gradient of 2060 x 7176 over 272: M 26, S 31, B 33, D 33, L 34; 16 x 7168 x 2048, the sum split by 4: S 14.4, D 16, M 18, L 24; weight gradients of 2048 x 2048 over
+// 512 tokens: M 12.9, B 13.2, W 15.6, L 19.7; of 2368 x 7168 over 333: W 27, M 30, B 33, L 35.
 struct CfgL {                // 8 waves of 128 x 64, alternating
     static constexpr int BR = 256, BC = 256, WR = 2, WC = 4, kStages = 2;
     static constexpr bool kAlternate = true;
@@ -40,6 +51,10 @@ struct CfgW {                // as M with one buffer and one set of operands: fo
 };
 struct CfgD {                // as M with a step more in flight, one workgroup a CU
     static constexpr int BR = 128, BC = 128, WR = 2, WC = 2, kStages = 3;
+    static constexpr bool kAlternate = false;
+};
+struct CfgB {                // 8 waves of 64 x 64: half the misses of D for the columns operand of a product
+    static constexpr int BR = 256, BC = 128, WR = 4, WC = 2, kStages = 3;
     static constexpr bool kAlternate = false;
 };
 
@@ -576,6 +591,7 @@ template <int FORM, class Epi>
 moe_status dense_run(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s,
                      const DenseSide &side = {}) {
     if (pl.cfg == kTileL) return dense_run_cfg<CfgL, FORM>(p, pl, e, part, side, s);
+    if (pl.cfg == kTileB) return dense_run_cfg<CfgB, FORM>(p, pl, e, part, side, s);
     if constexpr (FORM == kFormTN) {
         if (pl.cfg == kTileW) return dense_run_cfg<CfgW, FORM>(p, pl, e, part, side, s);
     } else {

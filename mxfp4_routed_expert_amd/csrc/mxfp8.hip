@@ -4,7 +4,8 @@
 // Conversion of a block (OCP Microscaling Formats v1.0): X = floor(log2 amax) - 8 (8 = the largest
 // E4M3 exponent), kept in [-127, 127]; codes are the nearest E4M3 values of v / 2^X, ties to even,
 // saturating at 448.  Both directions move 3 and 1/32 bytes a bf16 value and are bound by HBM: a
-// lane takes 8 values, four neighbouring lanes a block.
+// lane takes 8 values, four neighbouring lanes a block.  8192 x 7168 (178 MB): 31.7 us to codes (5.6 TB/s),
+// 26.5 back (6.7 TB/s, the codes partly in the last-level cache); 1024 x 6144: 5.5 and 8.5 us.
 #include "dense.h"
 
 namespace moe {

@@ -321,19 +321,22 @@ def test_block_of_no_tokens(M, checkpoint):
     assert dx.shape == (0, 64) and all((g == 0).all() for g in dws)
 
 
-# (rows, columns, sum) at which the forward and input-gradient products take each tile shape (256 x 256, 128 x 128 in
-# its two forms, 64 x 128) with the sum whole, split for the tiles of a last partial round, and split everywhere
+# (rows, columns, sum) at which the forward and input-gradient products take each tile shape (256 x 256, 256 x 128,
+# 128 x 128 in its two forms, 64 x 128) with the sum whole, split for the tiles of a last partial round, and split everywhere
 TILES = [(9, 264, 136), (260, 7176, 136), (260, 7176, 328), (1030, 7176, 136), (9, 264, 1160), (70, 2056, 2376), (130, 7176, 4104),
-         (4100, 264, 7176), (520, 7176, 2376), (1030, 4104, 2376), (2060, 7176, 1160), (1100, 7176, 2376)]
+         (4100, 264, 7176), (520, 7176, 2376), (1030, 4104, 2376), (2060, 7176, 1160), (1100, 7176, 2376),
+         (130, 4104, 2056), (1100, 7176, 2056), (520, 7176, 136), (520, 7176, 7176), (520, 4104, 7176)]
 # the gated products' (tokens, d_ff, d_model)
 PAIR_TILES = [(9, 264, 136), (130, 7176, 136), (130, 7176, 328), (520, 7176, 136), (9, 264, 1160), (70, 1032, 2376), (130, 4104, 4104),
-              (700, 1032, 7176), (260, 7176, 2376), (1030, 2056, 2376), (2060, 7176, 520), (4100, 1032, 4104)]
+              (700, 1032, 7176), (260, 7176, 2376), (1030, 2056, 2376), (2060, 7176, 520), (4100, 1032, 4104),
+              (130, 2056, 2056), (4100, 1032, 2056), (260, 7176, 136), (130, 4104, 7176), (4100, 2056, 1160)]
 # input gradients of the gated products (tokens, d_model, d_ff): a sum of two parts
 TWO_PART_TILES = [(70, 264, 136), (260, 7176, 136), (1030, 7176, 136), (70, 264, 520), (70, 2056, 1160), (130, 7176, 2376),
-                  (520, 7176, 1160), (1030, 4104, 1160), (4100, 4104, 328)]
+                  (520, 7176, 1160), (1030, 4104, 1160), (4100, 4104, 328), (130, 4104, 1160), (1030, 7176, 1160), (520, 7176, 136),
+                  (520, 7176, 2376), (130, 7176, 7176), (520, 4104, 2376), (2060, 7176, 136)]
 # weight gradients (tokens, n, k)
 GRAD_TILES = [(9, 1032, 7176), (70, 4104, 7176), (520, 264, 136), (1030, 1032, 7176), (5200, 264, 7176), (5200, 2376, 1160),
-              (1030, 4104, 4104), (2600, 4104, 4104)]
+              (1030, 4104, 4104), (2600, 4104, 4104), (1030, 7176, 520), (4100, 7176, 1160), (4100, 2056, 7176), (9, 264, 136)]
 
 
 def rnd_gpu(seed, *shape, std=1.0, dtype=bf16):
