@@ -381,12 +381,14 @@ moe_status moe_mx_quantize(int32_t rows, int32_t cols, const void *x, int32_t x_
  * Dense bf16 layers: the feed-forward block that runs on every token beside the routed experts
  * (the dense layers and a bf16 shared expert: rabbit README, design section and architecture
  * table), and its gradients.  For all of them: weights bf16, row-major [n][kdim]; biases float32;
- * sums, activations and bias gradients in float32; every matrix has fewer than 2^31 elements;
- * tensors 16-byte aligned; kdim, d_model and d_ff multiples of 8.  A NaN or infinity reaches
- * the outputs whose sums it takes part in, and no others.  Results depend on the arguments alone:
- * the same call gives the same bits (sums have a fixed order; no atomics).  The workspace is
- * 16-byte aligned; calls that may run at the same time (other streams, other captured graphs)
- * need one each.
+ * sums, activations and bias gradients in float32; every matrix has fewer than 2^31 elements (with
+ * up to 64 tokens, the terms that a value is kept as counted together); tensors 16-byte aligned,
+ * outputs apart from inputs and from each other unless a call says otherwise; kdim, d_model and
+ * d_ff multiples of 8.  A NaN or infinity reaches the outputs whose sums it takes part in, and no
+ * others (an infinity may arrive as NaN where it meets a value kept as several terms, some of them
+ * 0).  Results depend on the arguments alone: the same call gives the same bits (sums have a fixed
+ * order; no atomics).  The workspace is 16-byte aligned; calls that may run at the same time (other
+ * streams, other captured graphs) need one each.
  *
  * moe_dense_linear -- y = f(x W^T + bias) + residual.
  *   x [T][kdim] of x_dtype (bf16 or float32), W [n][kdim], bias [n] or NULL, residual [T][n] of
@@ -400,8 +402,8 @@ moe_status moe_mx_quantize(int32_t rows, int32_t cols, const void *x, int32_t x_
  *   x is bf16 or float32, or MXFP8 codes with x_scales (x_dtype MOE_DT_MXFP8, kdim a multiple of 32):
  *   the 8-bit checkpoint stands for x everywhere, also in z.  z is recomputed when fn is not
  *   MOE_FN_NONE.  For dx and dw, dz is rounded to bf16 (the matrix cores' operand type) when T > 64
- *   and kept as two bf16 terms up to there; dbias sums the unrounded values.  Any of dx, dw, dbias
- *   may be NULL (not wanted), not all.  The residual's gradient is dy.
+ *   and kept as two bf16 terms up to there; dbias sums the unrounded values.  A float32 x enters dw as
+ *   its two leading bf16 terms (within 2^-16).  Any of dx, dw, dbias may be NULL (not wanted), not all.  The residual's gradient is dy.
  *   x may be NULL when fn is MOE_FN_NONE and dw is NULL; w when fn is MOE_FN_NONE and dx is NULL.
  *   bias is read only when fn is not MOE_FN_NONE.  y_dtype is ignored.
  *   With T == 0 dw and dbias are written as zeros, and nothing need be asked for.

@@ -29,10 +29,14 @@
 
 namespace moe {
 
-// The shapes, with sizes at which each is the fastest (us, operands from HBM).  4093 x 7168 x 2048: L 115, B 128, M
-// 148, D 157, S 163; 1024 x 7168 x 2048: B 34.5, M 40, D 46, S 52, L 56; 512 x 7168 x 2368: D 28, S 34, B 36,
-// M 39, L 63; input gradient of 2060 x 7176 over 272: M 26, S 31, B 33, D 33, L 34; 16 x 7168 x 2048, the sum split by 4: S 14.4, D 16, M 18, L 24; weight gradients of 2048 x 2048 over
-// 512 tokens: M 12.9, B 13.2, W 15.6, L 19.7; of 2368 x 7168 over 333: W 27, M 30, B 33, L 35.
+// The shapes, with sizes at which each is the fastest (us, operands from HBM):
+//   4093 x 7168 x 2048                              L 115  B 128  M 148  D 157  S 163
+//   1024 x 7168 x 2048                              B 34.5  M 40  D 46  S 52  L 56
+//   512 x 7168 x 2368                               D 28  S 34  B 36  M 39  L 63
+//   input gradient, 2060 x 7176 x 272               M 26  S 31  B 33  D 33  L 34
+//   16 x 7168 x 2048, the sum split by 4            S 14.4  D 16  M 18  L 24
+//   weight gradient, 2048 x 2048 over 512 tokens    M 12.9  B 13.2  W 15.6  L 19.7
+//   weight gradient, 2368 x 7168 over 333 tokens    W 27  M 30  B 33  L 35
 struct CfgL {                // 8 waves of 128 x 64, alternating
     static constexpr int BR = 256, BC = 256, WR = 2, WC = 4, kStages = 2;
     static constexpr bool kAlternate = true;
