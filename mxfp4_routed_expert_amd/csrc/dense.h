@@ -463,13 +463,69 @@ moe_status dense_linear_bwd_product(const DenseProduct &p, const DensePlan &pl, 
 moe_status dense_gate_bwd_product(const DenseProduct &p, const DensePlan &pl, const EpiGateBwd &e, float *part,
                                   hipStream_t s);
 
-// Sum the parts of the split tiles and run the epilogue on the sums (dense_aux.hip).  br x bc: the tile.
-// Partial results: [split tile][part][br][bc], a pair tile's columns gate first.
-template <class Epi>
-moe_status dense_finish(const DenseProduct &p, const DensePlan &pl, int br, int bc, const Epi &e, const float *part,
-                        hipStream_t s);
+// The split tiles' parts.  Partial results: [split tile][part][br][bc], a pair tile's columns gate first.
+struct DenseParts {
+    const float *part;
+    int full, split, terms, tr, tc, rows, C, br, lanes;   // lanes: threads a row, four columns (of each matrix) each
+    int wgs;                                              // workgroups that sum them, kFinishRows rows of a tile each
+};
 constexpr int kFinishRows = 16;   // rows per workgroup there, and per column-sum row of the launch
 constexpr int kSavedRows = 2;     // rows per workgroup of the saved pre-activations' gradients
+
+// Sum the parts of the split tiles in order (the same order on every run), the terms of a row after each
+// other, and run the epilogue.  Workgroup `wg` of 256 threads takes kFinishRows rows of a tile; LANES threads a
+// row, four columns each, and a thread U rows, whose loads of all parts are independent.
+constexpr int kFinishThreads = 256;
+struct FinishPlace {
+    int row, c;                                           // the workgroup's index along the rows; the thread's column
+};
+template <int LANES, class Epi>
+MOE_DEV FinishPlace dense_finish_rows(const DenseParts &q, const Epi &epi, int wg, f32x4 &sa, f32x4 &sb) {
+    constexpr int kStep = kFinishThreads / LANES, U = kFinishRows / kStep;
+    constexpr int BC = LANES * 4 * (Epi::kPair ? 2 : 1);
+    static_assert(U >= 1 && U * kStep == kFinishRows, "whole rows");
+    const int blocks = q.br / kFinishRows;
+    const int t = wg / blocks, rb = wg - t * blocks;
+    int tr, tc;
+    if (q.terms == 1) {
+        tile_at(q.full + t, q.tr, q.tc, tr, tc);
+    } else {                                      // (every tile is split) output rows are the first term's
+        tr = t / q.tc;
+        tc = t - tr * q.tc;
+    }
+    const int lane = threadIdx.x % LANES, er = threadIdx.x / LANES;
+    const int c = tc * (LANES * 4) + 4 * lane, r = tr * q.br + rb * kFinishRows + er;
+    if (c < q.C && r < q.rows) {
+        f32x4 a[U], b[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) a[u] = b[u] = kZero4;
+        for (int j = 0; j < q.terms; ++j) {
+            const float *src[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int rr = min(r + u * kStep, q.rows - 1) + j * q.rows, rt = rr / q.br;
+                src[u] = q.part + ((size_t)(tile_slot(rt, tc, q.tr, q.tc) - q.full) * q.split * q.br + (rr - rt * q.br)) * BC +
+                         4 * lane;
+            }
+            for (int s = 0; s < q.split; ++s)
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const float *p = src[u] + (size_t)s * q.br * BC;
+                    a[u] += *(const f32x4 *)p;
+                    if constexpr (Epi::kPair) b[u] += *(const f32x4 *)(p + BC / 2);
+                }
+        }
+        epi.rows(epi.cols(c), r, kStep, q.rows, c, a, b, sa, sb);
+    }
+    return FinishPlace{tr * blocks + rb, c};
+}
+// ... as a launch (dense_aux.hip), or, for a product's plain results, beside a later product (DenseLater)
+template <class Epi>
+moe_status dense_finish(const DenseParts &q, const Epi &e, hipStream_t s);
+struct DenseLater {
+    DenseParts q;                                         // q.wgs == 0: nothing
+    EpiStore e;
+};
 
 // Column sums, in two steps of a fixed order: partial sums of kColRows rows of a bf16 matrix [rows][C]
 // (kSideSum: out0 [ceil(rows / kColRows)][ld]), and the sum of partial rows [rows][ld] (kSideReduce: columns
@@ -530,10 +586,12 @@ MOE_DEV void dense_side_job(const DenseSide &j, int wg, float *lds) {
     }
 }
 moe_status dense_side_launch(const DenseSide &j, hipStream_t s);
+// later: NULL, or where to leave the sum of the split tiles, for the next product
 moe_status dense_nn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, const DenseSide &side,
-                            hipStream_t s);
+                            DenseLater *later, hipStream_t s);
+// later: what an input gradient left, summed beside this product's W tiles
 moe_status dense_tn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, const DenseSide &side,
-                            hipStream_t s);
+                            const DenseLater &later, hipStream_t s);
 // Gradients of the gated product from saved pre-activations [2][R][C] (dense_aux.hip).
 moe_status dense_gate_bwd_saved(const EpiGateBwd &e, const uint16_t *pre, int R, hipStream_t s);
 // float32 rows [n] -> three bf16 planes [3][n] whose sum is the value exactly.

@@ -20,67 +20,30 @@ MOE_DEV Block block_of(int C) {
 }
 dim3 block_grid(int R, int rows, int C) { return dim3((unsigned)((R + rows - 1) / rows) * (unsigned)col_blocks(C)); }
 
-// Sum the parts of the split tiles in order (the same order on every run), the terms of a row after each
-// other, and run the epilogue.  A workgroup takes kFinishRows rows of a tile; LANES threads a row, four
-// columns each, and a thread U rows, whose loads of all parts are independent.  Bound by the partial results,
-// written just before and read from the last-level cache: gate and up of 512 x 2368, six parts (60 MB), 10.7
-// us, 5.6 TB/s; five parts of 61 x 6144, two terms (16 MB), 6.3 us, half of it the launch.  (Loads of four
-// parts at a time measured the same.)
+// Sum the parts of the split tiles.  Bound by the partial results, written just before and read from the last-level
+// cache: gate and up of 512 x 2368, six parts (60 MB), 10.7 us, 5.6 TB/s; five parts of 61 x 6144, two terms (16
+// MB), 6.3 us, half of it the launch.  (Loads of four parts at a time measured the same.)
 template <int LANES, class Epi>
-__global__ __launch_bounds__(kThreads) void dense_finish_kernel(const float *__restrict__ part, int full, int split, int terms,
-                                                                int tr_n, int tc_n, int rows, int C, int br, Epi epi) {
-    constexpr int kStep = kThreads / LANES, U = kFinishRows / kStep;
-    constexpr int BC = LANES * 4 * (Epi::kPair ? 2 : 1);
-    static_assert(U >= 1 && U * kStep == kFinishRows, "whole rows");
-    const int blocks = br / kFinishRows;
-    const int t = blockIdx.x / blocks, rb = blockIdx.x - t * blocks;
-    int tr, tc;
-    if (terms == 1) {
-        tile_at(full + t, tr_n, tc_n, tr, tc);
-    } else {                                      // (every tile is split) output rows are the first term's
-        tr = t / tc_n;
-        tc = t - tr * tc_n;
-    }
-    const int lane = threadIdx.x % LANES, er = threadIdx.x / LANES;
-    const int c = tc * (LANES * 4) + 4 * lane, r = tr * br + rb * kFinishRows + er;
-    const bool live = c < C && r < rows;
+__global__ __launch_bounds__(kFinishThreads) void dense_finish_kernel(const DenseParts q, Epi epi) {
+    constexpr int kStep = kFinishThreads / LANES;
     f32x4 sa = kZero4, sb = kZero4;
-    if (live) {
-        f32x4 a[U], b[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) a[u] = b[u] = kZero4;
-        for (int j = 0; j < terms; ++j) {
-            const float *src[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int rr = min(r + u * kStep, rows - 1) + j * rows, rt = rr / br;
-                src[u] = part + ((size_t)(tile_slot(rt, tc, tr_n, tc_n) - full) * split * br + (rr - rt * br)) * BC + 4 * lane;
-            }
-            for (int s = 0; s < split; ++s)
-#pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    const float *q = src[u] + (size_t)s * br * BC;
-                    a[u] += *(const f32x4 *)q;
-                    if constexpr (Epi::kPair) b[u] += *(const f32x4 *)(q + BC / 2);
-                }
-        }
-        epi.rows(epi.cols(c), r, kStep, rows, c, a, b, sa, sb);
-    }
+    const FinishPlace at = dense_finish_rows<LANES>(q, epi, blockIdx.x, sa, sb);
     if constexpr (Epi::kColSum) {
         if (epi.cs) {
             // column sums of the workgroup's rows, one partial row
             __shared__ f32x4 s_sum[Epi::kPair ? 2 : 1][kStep][LANES];
+            const int lane = threadIdx.x % LANES, er = threadIdx.x / LANES;
             s_sum[0][er][lane] = sa;
             if constexpr (Epi::kPair) s_sum[1][er][lane] = sb;
             __syncthreads();
-            if (er == 0 && c < C) {
+            if (er == 0 && at.c < q.C) {
                 for (int i = 1; i < kStep; ++i) {
                     sa += s_sum[0][i][lane];
                     if constexpr (Epi::kPair) sb += s_sum[1][i][lane];
                 }
-                float *row = epi.cs + (size_t)(tr * blocks + rb) * epi.csld;
-                *(f32x4 *)(row + c) = sa;
-                if constexpr (Epi::kPair) *(f32x4 *)(row + C + c) = sb;
+                float *row = epi.cs + (size_t)at.row * epi.csld;
+                *(f32x4 *)(row + at.c) = sa;
+                if constexpr (Epi::kPair) *(f32x4 *)(row + q.C + at.c) = sb;
             }
         }
     }
@@ -156,31 +119,20 @@ __global__ __launch_bounds__(kThreads) void pad_rows_kernel(const uint16_t *__re
 }  // namespace
 
 template <class Epi>
-moe_status dense_finish(const DenseProduct &p, const DensePlan &pl, int br, int bc, const Epi &e, const float *part,
-                        hipStream_t s) {
-    const int rows = p.R / p.terms, blocks = br / kFinishRows;
-    const int tiles = p.terms == 1 ? pl.tr * pl.tc - pl.full : (rows + br - 1) / br * pl.tc;
-    const dim3 grid((unsigned)(tiles * blocks));
-    const int lanes = bc / 4 / (Epi::kPair ? 2 : 1);
-#define MOE_FINISH(L)                                                                                                    \
-    hipLaunchKernelGGL((dense_finish_kernel<L, Epi>), grid, dim3(kThreads), 0, s, part, pl.full, pl.split, p.terms, pl.tr, \
-                       pl.tc, rows, p.C, br, e)
-    if (lanes == 64) MOE_FINISH(64);
-    else if (lanes == 32) MOE_FINISH(32);
+moe_status dense_finish(const DenseParts &q, const Epi &e, hipStream_t s) {
+    const dim3 grid((unsigned)q.wgs);
+#define MOE_FINISH(L) hipLaunchKernelGGL((dense_finish_kernel<L, Epi>), grid, dim3(kFinishThreads), 0, s, q, e)
+    if (q.lanes == 64) MOE_FINISH(64);
+    else if (q.lanes == 32) MOE_FINISH(32);
     else MOE_FINISH(16);
 #undef MOE_FINISH
     return launch_check("dense product: sum of its parts");
 }
-template moe_status dense_finish<EpiLinear>(const DenseProduct &, const DensePlan &, int, int, const EpiLinear &, const float *,
-                                            hipStream_t);
-template moe_status dense_finish<EpiGate>(const DenseProduct &, const DensePlan &, int, int, const EpiGate &, const float *,
-                                          hipStream_t);
-template moe_status dense_finish<EpiLinearBwd>(const DenseProduct &, const DensePlan &, int, int, const EpiLinearBwd &,
-                                               const float *, hipStream_t);
-template moe_status dense_finish<EpiGateBwd>(const DenseProduct &, const DensePlan &, int, int, const EpiGateBwd &,
-                                             const float *, hipStream_t);
-template moe_status dense_finish<EpiStore>(const DenseProduct &, const DensePlan &, int, int, const EpiStore &, const float *,
-                                           hipStream_t);
+template moe_status dense_finish<EpiLinear>(const DenseParts &, const EpiLinear &, hipStream_t);
+template moe_status dense_finish<EpiGate>(const DenseParts &, const EpiGate &, hipStream_t);
+template moe_status dense_finish<EpiLinearBwd>(const DenseParts &, const EpiLinearBwd &, hipStream_t);
+template moe_status dense_finish<EpiGateBwd>(const DenseParts &, const EpiGateBwd &, hipStream_t);
+template moe_status dense_finish<EpiStore>(const DenseParts &, const EpiStore &, hipStream_t);
 
 moe_status dense_gate_bwd_saved(const EpiGateBwd &e, const uint16_t *pre, int R, hipStream_t s) {
     hipLaunchKernelGGL(gate_bwd_saved_kernel, block_grid(R, kSavedRows, e.C), dim3(kThreads), 0, s, pre, R, e);

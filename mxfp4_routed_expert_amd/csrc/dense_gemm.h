@@ -70,8 +70,9 @@ struct GemmArgs {
     int tr, tc, full, split, steps, seg_steps;
     int cs_sub;           // column-sum rows per wave row of a tile
     float *part;
-    int main_wgs;         // workgroups of the product; those past them run `side`
+    int main_wgs, side_wgs;   // workgroups of the product; the next ones run `side`, those past them `later`
     DenseSide side;
+    DenseLater later;
 };
 
 __device__ __attribute__((aligned(16))) const uint32_t g_dense_zero[4] = {0, 0, 0, 0};
@@ -129,7 +130,15 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, Cfg::kStages == 1 ? 4 : 2) v
 
     if constexpr (std::is_same_v<Epi, EpiStore>)
         if ((int)blockIdx.x >= ga.main_wgs) {
-            dense_side_job<64 * NW>(ga.side, blockIdx.x - ga.main_wgs, (float *)smem);
+            const int wg = blockIdx.x - ga.main_wgs;
+            if (wg < ga.side_wgs) {
+                dense_side_job<64 * NW>(ga.side, wg, (float *)smem);
+            } else if constexpr (Cfg::kStages == 1) {
+                static_assert(64 * NW == kFinishThreads, "as in the launch of its own");
+                f32x4 sa, sb;
+                if (ga.later.q.lanes == 64) dense_finish_rows<64>(ga.later.q, ga.later.e, wg - ga.side_wgs, sa, sb);
+                else dense_finish_rows<32>(ga.later.q, ga.later.e, wg - ga.side_wgs, sa, sb);
+            }
             return;
         }
     const DenseProduct &p = ga.p;
@@ -577,32 +586,43 @@ __global__ __launch_bounds__(64 * Cfg::WR *Cfg::WC, Cfg::kStages == 1 ? 4 : 2) v
     }
 }
 
-// The product with its epilogue, and the sum of its split tiles.
+// The product with its epilogue, and the sum of its split tiles: at once, or left in `leave`.  `later`: the one a
+// product before this left.
 template <class Cfg, int FORM, class Epi>
-moe_status dense_run_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, const DenseSide &side, hipStream_t s) {
-    constexpr int lds = Cfg::kStages * (Cfg::BR + Cfg::BC) * kBK * 2;
+moe_status dense_run_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, const DenseSide &side,
+                         DenseLater *leave, const DenseLater &later, hipStream_t s) {
+    constexpr int lds = Cfg::kStages * (Cfg::BR + Cfg::BC) * kBK * 2, kThreads = 64 * Cfg::WR * Cfg::WC;
     const int tiles = pl.tr * pl.tc;
     const bool tail = pl.full < tiles;
     GemmArgs ga{p, pl.tr, pl.tc, pl.full, pl.split, pl.steps, (p.K + kBK - 1) / kBK, tail ? Cfg::BR / Cfg::WR / kFinishRows : 1,
-                part, pl.full + (tiles - pl.full) * pl.split, side};
-    hipLaunchKernelGGL((dense_gemm_kernel<Cfg, FORM, Epi>), dim3((unsigned)(ga.main_wgs + dense_side_wgs(side, 64 * Cfg::WR * Cfg::WC))),
-                       dim3(64 * Cfg::WR * Cfg::WC), lds, s, ga, e);
+                part, pl.full + (tiles - pl.full) * pl.split, dense_side_wgs(side, kThreads), side, later};
+    hipLaunchKernelGGL((dense_gemm_kernel<Cfg, FORM, Epi>), dim3((unsigned)(ga.main_wgs + ga.side_wgs + later.q.wgs)), dim3(kThreads),
+                       lds, s, ga, e);
     MOE_TRY(launch_check("dense product"));
-    return tail ? dense_finish(p, pl, Cfg::BR, Cfg::BC, e, part, s) : MOE_OK;
+    if (!tail) return MOE_OK;
+    const int rows = p.R / p.terms, blocks = Cfg::BR / kFinishRows;
+    const int sums = p.terms == 1 ? tiles - pl.full : (rows + Cfg::BR - 1) / Cfg::BR * pl.tc;
+    const DenseParts q{part, pl.full, pl.split, p.terms, pl.tr, pl.tc, rows, p.C, Cfg::BR, Cfg::BC / 4 / (Epi::kPair ? 2 : 1), sums * blocks};
+    if constexpr (std::is_same_v<Epi, EpiStore>)
+        if (leave) {
+            *leave = DenseLater{q, e};
+            return MOE_OK;
+        }
+    return dense_finish(q, e, s);
 }
 
 template <int FORM, class Epi>
-moe_status dense_run(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s,
-                     const DenseSide &side = {}) {
-    if (pl.cfg == kTileL) return dense_run_cfg<CfgL, FORM>(p, pl, e, part, side, s);
-    if (pl.cfg == kTileB) return dense_run_cfg<CfgB, FORM>(p, pl, e, part, side, s);
+moe_status dense_run(const DenseProduct &p, const DensePlan &pl, const Epi &e, float *part, hipStream_t s, const DenseSide &side = {},
+                     DenseLater *leave = nullptr, const DenseLater &later = {}) {
+    if (pl.cfg == kTileL) return dense_run_cfg<CfgL, FORM>(p, pl, e, part, side, leave, later, s);
+    if (pl.cfg == kTileB) return dense_run_cfg<CfgB, FORM>(p, pl, e, part, side, leave, later, s);
     if constexpr (FORM == kFormTN) {
-        if (pl.cfg == kTileW) return dense_run_cfg<CfgW, FORM>(p, pl, e, part, side, s);
+        if (pl.cfg == kTileW) return dense_run_cfg<CfgW, FORM>(p, pl, e, part, side, leave, later, s);
     } else {
-        if (pl.cfg == kTileS) return dense_run_cfg<CfgS, FORM>(p, pl, e, part, side, s);
-        if (pl.cfg == kTileD) return dense_run_cfg<CfgD, FORM>(p, pl, e, part, side, s);
+        if (pl.cfg == kTileS) return dense_run_cfg<CfgS, FORM>(p, pl, e, part, side, leave, later, s);
+        if (pl.cfg == kTileD) return dense_run_cfg<CfgD, FORM>(p, pl, e, part, side, leave, later, s);
     }
-    return dense_run_cfg<CfgM, FORM>(p, pl, e, part, side, s);
+    return dense_run_cfg<CfgM, FORM>(p, pl, e, part, side, leave, later, s);
 }
 
 }  // namespace moe

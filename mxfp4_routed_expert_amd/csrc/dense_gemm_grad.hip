@@ -5,12 +5,12 @@
 namespace moe {
 
 moe_status dense_nn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, const DenseSide &side,
-                            hipStream_t s) {
-    return dense_run<kFormNN>(p, pl, e, part, s, side);
+                            DenseLater *later, hipStream_t s) {
+    return dense_run<kFormNN>(p, pl, e, part, s, side, later);
 }
 moe_status dense_tn_product(const DenseProduct &p, const DensePlan &pl, const EpiStore &e, float *part, const DenseSide &side,
-                            hipStream_t s) {
-    return dense_run<kFormTN>(p, pl, e, part, s, side);
+                            const DenseLater &later, hipStream_t s) {
+    return dense_run<kFormTN>(p, pl, e, part, s, side, nullptr, later);
 }
 
 }  // namespace moe
