@@ -21,6 +21,10 @@ MOE_DEV uint32_t pack2_bf16(float a, float b) {
 MOE_DEV void store4_bf16(uint16_t *p, const f32x4 v) {
     *(u32x2 *)p = u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])};
 }
+// results that no kernel of the call reads: past the L2's lines (see EpiStore)
+MOE_DEV void stream4_bf16(uint16_t *p, const f32x4 v) {
+    __builtin_nontemporal_store(u32x2{pack2_bf16(v[0], v[1]), pack2_bf16(v[2], v[3])}, (u32x2 *)p);
+}
 MOE_DEV f32x4 load4_bf16(const uint16_t *p) {
     const u32x2 w = *(const u32x2 *)p;
     const f32x2 a = bf16x2_to_f32x2(w[0]), b = bf16x2_to_f32x2(w[1]);
@@ -381,7 +385,9 @@ struct EpiGateBwd {
 };
 
 // The product itself: rows below rows0 to out0, the others to out1 (the gate's and up's gradients).
-// C is a multiple of 8.
+// C is a multiple of 8.  Gradients leave as streaming stores, which keep the operands in the L2: weight gradients
+// of 4096 x 6144 over 1024 tokens 62.7 -> 55.7 us, of 2368 x 7168 over 333 27.3 -> 25.3.  (The forward passes'
+// results measured the same either way, partial results and checkpoints worse.)
 struct EpiStore {
     static constexpr bool kPair = false, kColSum = false;
     void *out0, *out1;
@@ -398,8 +404,8 @@ struct EpiStore {
             if (row >= R) continue;
             void *p = row < rows0 ? out0 : out1;
             const size_t o = (size_t)(row < rows0 ? row : row - rows0) * C + c;
-            if (f32) *(f32x4 *)((float *)p + o) = a[u];
-            else store4_bf16((uint16_t *)p + o, a[u]);
+            if (f32) __builtin_nontemporal_store(a[u], (f32x4 *)((float *)p + o));
+            else stream4_bf16((uint16_t *)p + o, a[u]);
         }
     }
 };
