@@ -11,7 +11,7 @@ constexpr int kCUs = 256;            // the plan is a pure function of the sizes
 // of a tile's start and end.  Fitted to 2900 timings of the four products over 16 to 4096 rows, 1000 to
 // 7168 columns and sums of 32 to 7168 values, operands not in the caches, every shape and split forced in
 // turn; there the plan's choice takes 0.5% longer than the fastest on average (weight gradients 2.3%) and
-// 15% at most (with the 256 x 128 tile, timed on 26 shapes: 1% and 6%).  A weight gradient's sum is short and
+// 15% at most (with the 256 x 128 tile, timed on 26 shapes, and streaming stores: 1% and 7%).  A weight gradient's sum is short and
 // its result large, hence costs of its own.
 struct Tile {
     int br, bc, wr, per_cu;
@@ -34,7 +34,7 @@ constexpr TileCosts kWeightGradCosts = {{{256, 256, 2, 1, 1.26, 5.7},
                                          {128, 128, 2, 2, 0.91, 3.0},
                                          {64, 128, 1, 2, 0.0, 0.0},
                                          {128, 128, 2, 1, 0.0, 0.0},
-                                         {128, 128, 2, 4, 1.65, 5.2},
+                                         {128, 128, 2, 4, 1.65, 4.6},
                                          {256, 128, 4, 1, 0.70, 5.9}},
                                         0.30, 2.0, 6.7e6};
 constexpr int kMaxSplit = 8;

@@ -36,7 +36,7 @@ namespace moe {
 //   input gradient, 2060 x 7176 x 272               M 26  S 31  B 33  D 33  L 34
 //   16 x 7168 x 2048, the sum split by 4            S 14.4  D 16  M 18  L 24
 //   weight gradient, 2048 x 2048 over 512 tokens    M 12.9  B 13.2  W 15.6  L 19.7
-//   weight gradient, 2368 x 7168 over 333 tokens    W 27  M 30  B 33  L 35
+//   weight gradient, 2368 x 7168 over 333 tokens    W 25  M 28  B 31  L 33
 struct CfgL {                // 8 waves of 128 x 64, alternating
     static constexpr int BR = 256, BC = 256, WR = 2, WC = 4, kStages = 2;
     static constexpr bool kAlternate = true;

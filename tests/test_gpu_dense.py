@@ -336,7 +336,7 @@ TWO_PART_TILES = [(70, 264, 136), (260, 7176, 136), (1030, 7176, 136), (70, 264,
                   (520, 7176, 2376), (130, 7176, 7176), (520, 4104, 2376), (2060, 7176, 136)]
 # weight gradients (tokens, n, k)
 GRAD_TILES = [(9, 1032, 7176), (70, 4104, 7176), (520, 264, 136), (1030, 1032, 7176), (5200, 264, 7176), (5200, 2376, 1160),
-              (1030, 4104, 4104), (2600, 4104, 4104), (1030, 7176, 520), (4100, 7176, 1160), (4100, 2056, 7176), (9, 264, 136)]
+              (1030, 4104, 4104), (2600, 4104, 4104), (1030, 7176, 520), (4100, 7176, 1160), (4100, 2056, 7176), (9, 264, 136), (2056, 6152, 2056)]
 
 
 def rnd_gpu(seed, *shape, std=1.0, dtype=bf16):
