@@ -18,12 +18,12 @@
 // Values past the end of the sum are copied from a zero page (for both operands), rows past the
 // end of a matrix repeat its last row and their results are not stored.
 //
-// What bounds it.  A step of the 256 x 256 tile takes 0.85 us of matrix instructions per CU and as much of
-// LDS bandwidth; it measures 1.05 - 1.15 us with its operands in the last-level cache (4096 x 4096 x 8192:
-// 182 us, 1.51 PFLOP/s) and 1.3 - 1.4 from HBM.  A step of a 128 x 128 tile measures 0.41 us from the
-// last-level cache and 0.58 from HBM: a CU's misses in flight are limited, to 47 bytes a ns from HBM and 77
-// from the last-level cache against 115 of L2 hits, however many copies are issued ahead (four and five
-// stages measured the same as three).
+// What bounds it.  A step of the 256 x 256 tile is 2048 cycles of matrix instructions, 1.0 - 1.1 us at the 1.9 -
+// 2.1 GHz that the card holds under them; it measures 1.05 - 1.15 us with its operands in the last-level cache (4096
+// x 4096 x 8192: 182 us, 1.51 PFLOP/s) and 1.3 - 1.4 from HBM.  A step of a 128 x 128 tile (512 cycles) measures
+// 0.41 us from the last-level cache and 0.58 from HBM: a CU's misses in flight are limited, to 47 bytes a ns from
+// HBM and 77 from the last-level cache against 115 of L2 hits, however many copies are issued ahead (four and
+// five stages measured the same as three).
 #pragma once
 #include "dense.h"
 
