@@ -547,7 +547,7 @@ struct DenseSide {
 // workgroups of `threads` threads that a job takes
 inline int dense_side_wgs(const DenseSide &j, int threads) {
     if (j.kind == kSideSum) return (j.rows + kColRows - 1) / kColRows * ((j.C + 4 * threads - 1) / (4 * threads));
-    if (j.kind == kSideReduce) return ((j.out1 ? 2 : 1) * j.C + 63) / 64;
+    if (j.kind == kSideReduce) return ((j.out1 ? 2 : 1) * j.C + threads / 4 - 1) / (threads / 4);
     return 0;
 }
 // workgroup `wg` of a job; lds: 64 floats a wave
@@ -572,10 +572,12 @@ MOE_DEV void dense_side_job(const DenseSide &j, int wg, float *lds) {
         *(f32x4 *)(j.out0 + (size_t)rb * j.ld + c) = s;
         return;
     }
-    // 64 columns a workgroup; each wave sums its share of the rows, the waves' sums are joined in order
-    constexpr int W = THREADS / 64;
-    const int lane = lane_id(), w = wave_id();
-    const int C = (j.out1 ? 2 : 1) * j.C, c = wg * 64 + lane;
+    // 64 columns for four waves; each sums its share of the rows, the four sums are joined in order (the same one in
+    // workgroups of any size)
+    constexpr int W = 4;
+    static_assert(THREADS % (64 * W) == 0, "whole groups of waves");
+    const int lane = lane_id(), w = wave_id() % W, group = wave_id() / W;
+    const int C = (j.out1 ? 2 : 1) * j.C, c = (wg * (THREADS / (64 * W)) + group) * 64 + lane;
     const int lo = (int)((int64_t)j.rows * w / W), hi = (int)((int64_t)j.rows * (w + 1) / W);
     const float *part = (const float *)j.in;
     float s = 0.0f;
@@ -583,6 +585,7 @@ MOE_DEV void dense_side_job(const DenseSide &j, int wg, float *lds) {
 #pragma unroll 8
         for (int r = lo; r < hi; ++r) s += part[(size_t)r * j.ld + c];
     }
+    lds += group * (64 * W);
     lds[w * 64 + lane] = s;
     __syncthreads();
     if (w == 0 && c < C) {

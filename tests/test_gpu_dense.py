@@ -312,6 +312,24 @@ def test_no_tokens(M):
     assert M.moe_mxfp8_quantize(x)[0].shape == (0, 64)
 
 
+# sizes at which a gradient's column sums and the sum of a split input gradient run beside the other product, and not
+@pytest.mark.parametrize("T,n,k", [(61, 2376, 1032), (333, 2368, 2056), (70, 264, 2056), (1030, 1032, 520), (2060, 2056, 1032)])
+@pytest.mark.parametrize("fn", ["none", "gelu"])
+def test_gradients_do_not_depend_on_what_else_is_asked(M, T, n, k, fn):
+    x, w, b, dy = rnd_gpu(1, T, k), rnd_gpu(2, n, k, std=k ** -0.5), rnd_gpu(3, n, dtype=f32), rnd_gpu(4, T, n)
+    every = M.moe_dense_linear_backward(dy, x, w, b, fn)
+    for want in (("dx",), ("dw",), ("dbias",), ("dx", "dw"), ("dx", "dbias"), ("dw", "dbias")):
+        for name, g, e in zip(("dx", "dw", "dbias"), M.moe_dense_linear_backward(dy, x, w, b, fn, want=want), every):
+            assert (g is None) == (name not in want) and (g is None or torch.equal(g, e)), (want, name)
+    wu, dh = rnd_gpu(5, n, k, std=k ** -0.5)[:n // 8 * 8], rnd_gpu(6, T, n // 8 * 8)
+    wg = w[:n // 8 * 8]
+    every = M.moe_dense_gateup_backward(dh, x, wg, wu, act_fn="silu")
+    for want in (("dx",), ("dw",), ("db",), ("dx", "dw"), ("dx", "db"), ("dw", "db")):
+        got = M.moe_dense_gateup_backward(dh, x, wg, wu, act_fn="silu", want=want)
+        for name, g, e in zip(("dx", "dw", "dw", "db", "db"), got, every):
+            assert (g is None) == (name not in want) and (g is None or torch.equal(g, e)), (want, name)
+
+
 @pytest.mark.parametrize("checkpoint", ["bf16", "mxfp8"])
 def test_block_of_no_tokens(M, checkpoint):
     ffn = M.DenseFFN(rnd(1, 40, 64), rnd(2, 40, 64), rnd(3, 64, 40), 0, checkpoint=checkpoint)
