@@ -51,7 +51,9 @@ MOE_DEV float rcp(float v) { return __builtin_amdgcn_rcpf(v); }
 
 // erfc(x) / 2 for x = |z| / sqrt 2, given E = exp(-z^2 / 2): E times a polynomial in t = 1 / (1 + 0.4 x)
 // (least-squares fit of erfc(x) exp(x^2) / 2 with equalised relative error, 1.3e-7 over x >= 0).  Phi is that for
-// negative z and 1 minus it otherwise: no cancellation on either side.
+// negative z and 1 minus it otherwise: no cancellation on either side, and the value keeps its relative accuracy
+// as far out as it is a normal number (z about -13).  A result rounded to bf16 takes it too: bf16 has float32's exponents, so
+// the tail is stored, and a gated h is scaled by u first.
 MOE_DEV float phi_of(float z, float E) {
     const float t = rcp(fmaf(0.28284271f, fabsf(z), 1.0f));
     float q = 0.025137422606348991f;
@@ -68,27 +70,8 @@ MOE_DEV float phi_of(float z, float E) {
 }
 MOE_DEV float gauss(float z) { return __builtin_amdgcn_exp2f((-0.5f * kLog2e) * z * z); }
 
-// z Phi(z) for a result rounded to bf16, as z s(t): Phi's logit t = ln(Phi / (1 - Phi)) is odd, here z times a polynomial in
-// z^2 up to 30 (least squares, weights equalising the error; in units of ln 2).  Off by at most 5e-7 in all,
-// and 1.7e-5 of the value down to z = -5: 2^-16, beside the rounding's 2^-8.  A shorter
-// chain than phi_of's: 4093 x 7168 x 2048 with bias takes 113.9 us instead of 118.1.
-MOE_DEV float gelu_bf16(float z) {
-    const float s = fminf(z * z, 30.0f);
-    float q = 1.4868742088253173e-12f;
-    q = fmaf(q, s, -2.3428767259581207e-10f);
-    q = fmaf(q, s, 1.586786169127663e-08f);
-    q = fmaf(q, s, -6.010500896991289e-07f);
-    q = fmaf(q, s, 1.3660417607752606e-05f);
-    q = fmaf(q, s, -0.00017099748947657645f);
-    q = fmaf(q, s, -6.566404044860974e-05f);
-    q = fmaf(q, s, 0.1048053428530693f);
-    q = fmaf(q, s, 2.3022186756134033f);
-    return z * rcp(1.0f + __builtin_amdgcn_exp2f(-z * q));
-}
-
-// to_bf16: the values go to bf16 next
 template <int U>
-MOE_DEV void act_rows(int fn, bool to_bf16, f32x4 (&a)[U]) {
+MOE_DEV void act_rows(int fn, f32x4 (&a)[U]) {
     auto each = [&](auto f) {
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -96,7 +79,6 @@ MOE_DEV void act_rows(int fn, bool to_bf16, f32x4 (&a)[U]) {
             for (int q = 0; q < 4; ++q) a[u][q] = f(a[u][q]);
     };
     if (fn == MOE_FN_SILU) each([](float z) { return z * rcp(1.0f + exp_neg(z)); });
-    else if (fn == MOE_FN_GELU && to_bf16) each([](float z) { return gelu_bf16(z); });
     else if (fn == MOE_FN_GELU) each([](float z) { return z * phi_of(z, gauss(z)); });
     else if (fn == MOE_FN_GELU_TANH) each([](float z) { return z * rcp(1.0f + exp_neg(gelu_arg(z))); });
     else if (fn == MOE_FN_RELU) each([](float z) { return z < 0.0f ? 0.0f : z; });
@@ -199,7 +181,7 @@ struct EpiLinear {
         if (res && vec) load_rows(add, res, y_f32, C, r, step, R, c);
 #pragma unroll
         for (int u = 0; u < U; ++u) a[u] += k.bias;
-        act_rows(fn, !y_f32 && !res, a);
+        act_rows(fn, a);
         if (vec) {
             if (res) {
 #pragma unroll
@@ -252,7 +234,7 @@ struct EpiGate {
             store_rows(a, pre, false, C, r, step, R, c);
             store_rows(b, pre + plane, false, C, r, step, R, c);
         }
-        act_rows(fn, !h_f32, a);
+        act_rows(fn, a);
 #pragma unroll
         for (int u = 0; u < U; ++u) a[u] *= b[u];
         store_rows(a, h, h_f32, C, r, step, R, c);
