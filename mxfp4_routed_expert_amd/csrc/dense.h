@@ -38,7 +38,7 @@ MOE_DEV uint16_t bf16_bits(float v) { return (uint16_t)(pack2_bf16(v, 0.0f) & 0x
 //   gelu       z Phi(z), Phi the normal distribution     f' = Phi + z exp(-z^2/2) / sqrt(2 pi)
 //   gelu_tanh  0.5 z (1 + tanh q) = z s(2q), q = sqrt(2/pi) (z + 0.044715 z^3): the logistic form
 //              has no cancellation for negative z         f' = s + z s (1 - s) 2q'
-//   relu       max(z, 0) (NaN stays NaN)                 f' = [z > 0]
+//   relu       max(z, 0)                                 f' = [z > 0]; NaN stays NaN in both
 // 1 - s is taken as e s with e = exp(-t), so it keeps its relative accuracy where s rounds to 1; there
 // e is held below infinity (as is z^2 in q'), so that a product with a zero stays zero for every finite z.
 constexpr float kLog2e = 1.4426950408889634f;
@@ -115,7 +115,7 @@ MOE_DEV void act_grad_rows(int fn, f32x4 (&z)[U], f32x4 (&d)[U]) {
         each([&](float &v, float &g) { logistic(v, gelu_arg(v), kGeluA + (3.0f * kGeluA * kGeluB) * fminf(v * v, 1e30f), g); });
     } else if (fn == MOE_FN_RELU) {
         each([](float &v, float &g) {
-            g = v > 0.0f ? 1.0f : 0.0f;
+            g = v > 0.0f ? 1.0f : (v <= 0.0f ? 0.0f : v);
             v = v < 0.0f ? 0.0f : v;
         });
     } else {

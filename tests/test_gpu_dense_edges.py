@@ -63,3 +63,68 @@ def test_activations_keep_their_relative_accuracy(M, fn, T):
         for p in (None, pre):
             again = M.moe_dense_gateup_backward(torch.ones_like(h), x, w, wu, act_fn=fn, pre=p, want=(), want_h=True, h_dtype=dt)[5]
             assert torch.equal(again, h), (fn, T, dt, p is None)
+
+
+def _spread(got, clean, where, what):
+    """NaN (or an infinity) exactly at `where` (a mask, or True / False for all / none); elsewhere the clean call's bits."""
+    m = where if isinstance(where, torch.Tensor) else torch.full_like(clean, where, dtype=torch.bool)
+    assert not torch.isfinite(got[m].float()).any(), f"{what}: {int(torch.isfinite(got[m].float()).sum())} of {int(m.sum())} values lost it"
+    assert torch.equal(got[~m], clean[~m]), f"{what}: it reached other values"
+
+
+def _at(t, *idx):
+    m = torch.zeros_like(t, dtype=torch.bool)
+    m[idx] = True
+    return m
+
+
+@pytest.mark.parametrize("T", [6, 20, 80, 300])
+@pytest.mark.parametrize("fn", ["none", "silu", "gelu", "gelu_tanh", "relu"])
+def test_nonfinite_values_in_linear_gradients(M, fn, T):
+    n, k, all_ = 72, 136, slice(None)
+    x, w, b, dy = rnd(1, T, k), rnd(2, n, k, std=k ** -0.5), rnd(3, n, dtype=f32), rnd(4, T, n)
+    run = lambda x=x, w=w, b=b, dy=dy: M.moe_dense_linear_backward(dy, x, w, b, fn)
+    cx, cw, cb = run()
+    put = lambda t, i, v=math.nan: t.clone().index_put_(tuple(torch.tensor(j) for j in i), torch.tensor(v, dtype=t.dtype, device="cuda"))
+    act = fn != "none"
+    # row 2 of x enters z's row 2, hence every sum over tokens; without an activation only dw's own column
+    dx, dw, db = run(x=put(x, (2, 5)))
+    _spread(dx, cx, _at(cx, 2) if act else False, "dx of x")
+    _spread(dw, cw, True if act else _at(cw, all_, 5), "dw of x")
+    _spread(db, cb, act, "dbias of x")
+    dx, dw, db = run(w=put(w, (70, 4)))
+    _spread(dx, cx, True if act else _at(cx, all_, 4), "dx of w")
+    _spread(dw, cw, _at(cw, 70) if act else False, "dw of w")
+    _spread(db, cb, _at(cb, 70) if act else False, "dbias of w")
+    dx, dw, db = run(b=put(b, (7,)))
+    for g, c, m in ((dx, cx, True), (dw, cw, _at(cw, 7)), (db, cb, _at(cb, 7))):
+        _spread(g, c, m if act else False, "bias")
+    for v in (math.nan, math.inf):
+        dx, dw, db = run(dy=put(dy, (2, 71), v))
+        for g, c, m in ((dx, cx, _at(cx, 2)), (dw, cw, _at(cw, 71)), (db, cb, _at(cb, 71))):
+            _spread(g, c, m, f"dy {v}")
+
+
+@pytest.mark.parametrize("T", [6, 80, 300])
+@pytest.mark.parametrize("fn", ["silu", "gelu", "gelu_tanh", "relu"])
+def test_nonfinite_values_in_gated_gradients(M, fn, T):
+    d, f = 136, 72
+    x, wg, wu, dh = rnd(1, T, d), rnd(2, f, d, std=d ** -0.5), rnd(3, f, d, std=d ** -0.5), rnd(4, T, f)
+    run = lambda wg=wg, wu=wu, pre=None: M.moe_dense_gateup_backward(dh, x, wg, wu, act_fn=fn, pre=pre, want_h=True)
+    put = lambda t, i: t.clone().index_put_(tuple(torch.tensor(j) for j in i), torch.tensor(math.nan, dtype=t.dtype, device="cuda"))
+    clean = run()
+    cx, cg, cu, cbg, cbu, ch = clean
+    col, names = slice(None), ("dx", "dw_gate", "dw_up", "db_gate", "db_up", "h")
+    # a gate weight: g's column, so dg, du and h there; an up weight: dg and h, while du = dh f(g) knows nothing of u
+    for got, masks, what in ((run(wg=put(wg, (70, 4))), (True, _at(cg, 70), _at(cu, 70), _at(cbg, 70), _at(cbu, 70), _at(ch, col, 70)), "w_gate"),
+                             (run(wu=put(wu, (70, 4))), (True, _at(cg, 70), False, _at(cbg, 70), False, _at(ch, col, 70)), "w_up")):
+        for g, c, m, name in zip(got, clean, masks, names):
+            _spread(g, c, m, f"{name} of {what}")
+    pre = M.moe_dense_gateup(x, wg, wu, act_fn=fn, want_pre=True)[1]
+    clean = run(pre=pre)
+    row = _at(clean[0], 2)
+    for i, up in ((0, _at(cu, 70)), (1, False)):
+        got = run(pre=put(pre, (i, 2, 70)))
+        masks = (row, _at(cg, 70), up, _at(cbg, 70), _at(cbu, 70) if i == 0 else False, _at(ch, 2, 70))
+        for g, c, m, name in zip(got, clean, masks, names):
+            _spread(g, c, m, f"{name} of saved {'gu'[i]}")
