@@ -393,7 +393,8 @@ moe_status moe_mx_quantize(int32_t rows, int32_t cols, const void *x, int32_t x_
  * moe_dense_linear -- y = f(x W^T + bias) + residual.
  *   x [T][kdim] of x_dtype (bf16 or float32), W [n][kdim], bias [n] or NULL, residual [T][n] of
  *   y_dtype or NULL (may be y itself), y [T][n] of y_dtype (bf16 or float32).  Any n >= 1.
- *   float32 x is used exactly: as float32 for T <= 8, else as three bf16 terms whose sum it is.
+ *   float32 x is used exactly: as float32 for T <= 8, else as three bf16 terms whose sum it is (what of it lies
+ *   below 2^-133, the smallest bf16, is cut off there).
  *   Ranges: up to 8 tokens read the weights once on the vector ALU and need no workspace; more run
  *   on the matrix cores, few tiles with the sum split over workgroups.
  * moe_dense_linear_backward -- with z = x W^T + bias and dz = dy f'(z):
@@ -403,7 +404,9 @@ moe_status moe_mx_quantize(int32_t rows, int32_t cols, const void *x, int32_t x_
  *   the 8-bit checkpoint stands for x everywhere, also in z.  z is recomputed when fn is not
  *   MOE_FN_NONE.  For dx and dw, dz is rounded to bf16 (the matrix cores' operand type) when T > 64
  *   and kept as two bf16 terms up to there; dbias sums the unrounded values.  A float32 x enters dw as
- *   its two leading bf16 terms (within 2^-16).  Any of dx, dw, dbias may be NULL (not wanted), not all.  The residual's gradient is dy.
+ *   its two leading bf16 terms (within 2^-16); where dz is two terms too, its second (within 2^-8 of it) meets x's
+ *   first (within 2^-7) alone: 2^-15 of a product more.  Any of dx, dw, dbias may be NULL (not wanted), not all.  The
+ *   residual's gradient is dy.
  *   x may be NULL when fn is MOE_FN_NONE and dw is NULL; w when fn is MOE_FN_NONE and dx is NULL.
  *   bias is read only when fn is not MOE_FN_NONE.  y_dtype is ignored.
  *   With T == 0 dw and dbias are written as zeros, and nothing need be asked for.

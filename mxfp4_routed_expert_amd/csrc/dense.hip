@@ -173,7 +173,8 @@ LinearWs linear_ws(const moe_linear_desc *d, void *base) {
 }
 
 // The sums of a linear layer's backward pass.  Up to kTermTokens tokens dz = dy f' is kept as two terms;
-// a float32 x is three terms for z and its two leading ones (2^-16) for dw, whose result is bf16.
+// a float32 x is three terms for z and its two leading ones (2^-16, and 2^-15 where dz's second term meets the
+// first alone) for dw, whose result is bf16.
 // The gradient products' partial results.  An input gradient's are summed beside the weight gradient's W tiles
 // where it takes those (four workgroups a CU, the sum's fit between; larger tiles would have to end first): the
 // weight gradient then has a place of its own for its parts.  61 tokens, 6144 x 2 x 2048: 46.9 -> 42.5 us, and

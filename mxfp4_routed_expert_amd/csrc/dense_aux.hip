@@ -72,8 +72,9 @@ __global__ __launch_bounds__(kThreads) void side_kernel(const DenseSide j) {
     dense_side_job<kThreads>(j, blockIdx.x, s_sum);
 }
 
-// v = hi + mid + lo exactly, each term the top eight significant bits of what is left
-// (truncation, so no term can round up past the largest finite bf16).  A non-finite v is its own
+// v = hi + mid + lo exactly (down to bf16's smallest value, 2^-133: what lies below is cut off).  hi is v's top eight significant
+// bits (truncated, so it cannot round up past the largest finite bf16), mid what is left rounded to nearest, so that hi +
+// mid alone is within 2^-16 of v on either side of it; lo is the rest, at most eight bits.  A non-finite v is its own
 // hi term and the others are zero.
 MOE_DEV void split3(float v, uint32_t &h, uint32_t &m, uint32_t &l) {
     const uint32_t u = __float_as_uint(v);
@@ -84,7 +85,8 @@ MOE_DEV void split3(float v, uint32_t &h, uint32_t &m, uint32_t &l) {
     }
     h = u >> 16;
     const float r1 = v - __uint_as_float(h << 16);
-    m = __float_as_uint(r1) >> 16;
+    const uint32_t b = __float_as_uint(r1);
+    m = (b + 0x7fffu + ((b >> 16) & 1u)) >> 16;              // ties to even; |r1| is below hi's last place: no overflow
     const float r2 = r1 - __uint_as_float(m << 16);
     l = __float_as_uint(r2) >> 16;
 }

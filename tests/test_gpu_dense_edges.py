@@ -128,3 +128,39 @@ def test_nonfinite_values_in_gated_gradients(M, fn, T):
         masks = (row, _at(cg, 70), up, _at(cbg, 70), _at(cbu, 70) if i == 0 else False, _at(ch, 2, 70))
         for g, c, m, name in zip(got, clean, masks, names):
             _spread(g, c, m, f"{name} of saved {'gu'[i]}")
+
+
+@pytest.mark.parametrize("T", [2, 9, 64, 100])
+def test_float32_rows_in_a_weight_gradient_are_within_two_terms(M, T):
+    # dw = x0 - x1 with x1 the value of x0's top 16 bits (two bf16 terms, exactly): what is left is x0's low byte, and x0's
+    # two leading terms are within 2^-16 of it; the bf16 rounding of the small difference and the sum's (two products a
+    # token and term, of which four are not zero) add little
+    k = 512
+    bits = torch.randint(0, 2 ** 23, (k,), generator=torch.Generator().manual_seed(1), dtype=torch.int32) + 0x3f800000
+    bits[:4] = torch.tensor([0x3f80ffff, 0x3f8000ff, 0x3fffffff, 0x3f800080], dtype=torch.int32)
+    x0 = bits.view(f32)
+    x = torch.zeros(T, k, dtype=f32)
+    x[0], x[1] = x0, (bits & -256).view(f32)
+    dy = torch.zeros(T, 8, dtype=bf16)
+    dy[0], dy[1] = 1, -1
+    w = rnd(2, 8, k)
+    dw = M.moe_dense_linear_backward(dy.cuda(), x.cuda(), w, want=("dw",))[1].double().cpu()
+    ref = x0.double() - x[1].double()
+    tol = 2.0 ** -16 * x0.double() + R.BF16 * (ref + 2.0 ** -16 * x0.double()) + 8 * R.EPS32 * 2 * x0.double()
+    worst = ((dw - ref).abs() / tol).max().item()
+    assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("T", [2, 12, 100])
+@pytest.mark.parametrize("xt", [bf16, f32])
+def test_small_rows_are_not_lost(M, T, xt):
+    # rows down to the smallest numbers against weights of 2^100: a bf16 value is one term, subnormal or not, and float32's
+    # terms end at 2^-133
+    k = 64
+    x, w = rnd(1, T, k, dtype=f32) * torch.exp2(-torch.arange(100, 100 + k, dtype=f32) * 0.5 - 60).cuda(), rnd(2, 24, k, std=0.1) * 2.0 ** 100
+    x = (x * 2.0 ** -6).to(xt)
+    y = M.moe_dense_linear(x, w, out_dtype=f32)
+    ref, tol = R.linear(x, w, None, "none", None, f32)
+    tol = tol + 2.0 ** -133 * w.double().abs().sum(1)
+    worst = ((y.double() - ref).abs() / tol).max().item()
+    assert worst <= 1, worst
