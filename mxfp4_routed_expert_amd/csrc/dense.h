@@ -424,7 +424,7 @@ struct DensePlan {
     int cfg;              // kTile*
     int tr, tc;           // tiles along rows and columns
     int full, split;
-    int steps;            // 64-value steps of the sum, all segments
+    int steps;            // 64-value steps of the sum, all segments; one a segment at least
     int cs_rows;          // column-sum partial rows the launch writes
     size_t part_bytes;    // partial results
 };

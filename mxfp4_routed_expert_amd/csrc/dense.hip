@@ -47,7 +47,7 @@ constexpr int kMaxSplit = 8;
 DensePlan dense_plan(int form, bool pair, int R, int C, int K, int nseg, int terms) {
     DensePlan best = {};
     double best_t = 1e30;
-    const int steps = (K + 63) / 64 * nseg;
+    const int steps = (K > 0 ? (K + 63) / 64 : 1) * nseg;     // (a sum of no values is one step of zeros)
     const int mats = pair ? 2 : 1;
     const TileCosts &costs = form == kFormTN ? kWeightGradCosts : kCosts;
     for (int cfg = 0; cfg < kTiles; ++cfg) {

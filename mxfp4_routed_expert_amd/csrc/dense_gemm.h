@@ -594,7 +594,7 @@ moe_status dense_run_cfg(const DenseProduct &p, const DensePlan &pl, const Epi &
     constexpr int lds = Cfg::kStages * (Cfg::BR + Cfg::BC) * kBK * 2, kThreads = 64 * Cfg::WR * Cfg::WC;
     const int tiles = pl.tr * pl.tc;
     const bool tail = pl.full < tiles;
-    GemmArgs ga{p, pl.tr, pl.tc, pl.full, pl.split, pl.steps, (p.K + kBK - 1) / kBK, tail ? Cfg::BR / Cfg::WR / kFinishRows : 1,
+    GemmArgs ga{p, pl.tr, pl.tc, pl.full, pl.split, pl.steps, pl.steps / p.nseg, tail ? Cfg::BR / Cfg::WR / kFinishRows : 1,
                 part, pl.full + (tiles - pl.full) * pl.split, dense_side_wgs(side, kThreads), side, later};
     hipLaunchKernelGGL((dense_gemm_kernel<Cfg, FORM, Epi>), dim3((unsigned)(ga.main_wgs + ga.side_wgs + later.q.wgs)), dim3(kThreads),
                        lds, s, ga, e);

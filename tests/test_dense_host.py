@@ -203,3 +203,25 @@ def test_binding_refuses_host_tensors():
                  lambda: B.moe_mxfp8_dequant(c, c[:, :2].contiguous())):
         with pytest.raises(ValueError, match="device memory"):
             call()
+
+
+class Plan(ctypes.Structure):
+    """DensePlan of csrc/dense.h."""
+    _fields_ = [(n, ctypes.c_int) for n in ("cfg", "tr", "tc", "full", "split", "steps", "cs_rows")] + [("part_bytes", ctypes.c_size_t)]
+
+
+FORWARD, INPUT_GRAD, WEIGHT_GRAD = range(3)
+
+
+def plan(form, rows, cols, k, nseg=1, terms=1, pair=False):
+    f = lib._ZN3moe10dense_planEibiiiii
+    f.restype, f.argtypes = Plan, [ctypes.c_int, ctypes.c_bool] + [ctypes.c_int] * 5
+    return f(form, pair, rows, cols, k, nseg, terms)
+
+
+@pytest.mark.parametrize("nseg", [1, 2, 3])
+def test_a_sum_of_no_tokens_has_a_step_in_every_segment(nseg):
+    # the product kernel finds a step's segment by dividing by the steps of one
+    for rows, cols in ((8, 8), (4096, 7168), (264, 136)):
+        assert plan(WEIGHT_GRAD, rows, cols, 0, nseg).steps == nseg
+        assert plan(WEIGHT_GRAD, rows, cols, 65, nseg).steps == 2 * nseg

@@ -164,3 +164,17 @@ def test_small_rows_are_not_lost(M, T, xt):
     tol = tol + 2.0 ** -133 * w.double().abs().sum(1)
     worst = ((y.double() - ref).abs() / tol).max().item()
     assert worst <= 1, worst
+
+
+@pytest.mark.parametrize("n,k", [(40, 64), (2375, 2056), (8200, 7176)])
+@pytest.mark.parametrize("xt", [bf16, f32])
+def test_weight_gradients_of_no_tokens_are_zeros(M, n, k, xt):
+    x, w, dy = torch.empty(0, k, dtype=xt, device="cuda"), rnd(1, n, k), torch.empty(0, n, dtype=bf16, device="cuda")
+    for fn in ("none", "gelu"):
+        dw, db = torch.full((n, k), math.nan, dtype=bf16, device="cuda"), torch.full((n,), math.nan, device="cuda")
+        M.moe_dense_linear_backward(dy, x, w, None, fn, want=("dw", "dbias"), out=(None, dw, db))
+        assert not dw.any() and not db.any()
+    f = n // 8 * 8
+    out = [torch.full(s, math.nan, dtype=t, device="cuda") for s, t in (((f, k), bf16), ((f, k), bf16), ((f,), f32), ((f,), f32))]
+    M.moe_dense_gateup_backward(dy[:, :f].contiguous(), x.to(bf16), w[:f], w[:f], want=("dw", "db"), out=(None, *out, None))
+    assert all(not t.any() for t in out)
