@@ -637,9 +637,16 @@ def _act_fn(name):
     return ACT_FN[name]
 
 
+def _int32(*sizes):
+    """Refuses what the C side's int32 cannot hold (ctypes would cut it off without a word)."""
+    if max(sizes) > 2 ** 31 - 1 or min(sizes) < -2 ** 31:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"sizes overflow int32 {sizes}")
+
+
 @functools.lru_cache(maxsize=4096)
 def _dense_plan(kind, *sizes):
     """(descriptor, workspace bytes) of a dense call: a function of its sizes and types alone."""
+    _int32(*sizes)
     d = ctypes.byref((LinearDesc if kind.startswith("linear") else GateupDesc)(*sizes))
     return d, getattr(lib, f"moe_dense_{kind}_workspace")(d)
 
@@ -788,6 +795,7 @@ def moe_mxfp8_quantize(x, out=None):
     """Rows of x (bf16 or float32, a multiple of 32 wide) as OCP MXFP8: (codes uint8 [rows][cols], E8M0 scales uint8
     [rows][cols/32]).  out: the two tensors."""
     rows, cols = _matrix(x, "x")
+    _int32(rows, cols)
     dev = x.device
     codes, scales = out if out is not None else (None, None)
     _operands(dev, (x, _one_of(x, DT), "x", None), (codes, torch.uint8, "codes", (rows, cols)),
@@ -802,6 +810,7 @@ def moe_mxfp8_quantize(x, out=None):
 def moe_mxfp8_dequant(codes, scales, out=None, out_dtype=torch.bfloat16):
     """The values of moe_mxfp8_quantize's codes and scales, bf16 or float32."""
     rows, cols = _matrix(codes, "codes")
+    _int32(rows, cols)
     dev = codes.device
     dt = out.dtype if out is not None else out_dtype
     if dt not in DT:

@@ -225,3 +225,22 @@ def test_a_sum_of_no_tokens_has_a_step_in_every_segment(nseg):
     for rows, cols in ((8, 8), (4096, 7168), (264, 136)):
         assert plan(WEIGHT_GRAD, rows, cols, 0, nseg).steps == nseg
         assert plan(WEIGHT_GRAD, rows, cols, 65, nseg).steps == 2 * nseg
+
+
+def test_sizes_past_int32_are_refused(monkeypatch):
+    # ctypes cuts an int off at 32 bits: 2^32 + 64 tokens would run as 64
+    big, bf, u8 = 2 ** 32 + 64, torch.bfloat16, torch.uint8
+    e = lambda *s, dt=bf: torch.empty(s, dtype=dt, device="meta")
+    monkeypatch.setattr(B, "_operands", lambda *a: None)
+    monkeypatch.setattr(B, "_launch", lambda *a: pytest.fail("launched with sizes past int32"))
+    w = e(64, 64)
+    for call in (lambda: B.moe_dense_linear_workspace(big, 64, 64, x_dtype=torch.float32), lambda: B.moe_dense_linear_workspace(64, 64, big),
+                 lambda: B.moe_dense_linear_backward_workspace(64, big, 64), lambda: B.moe_dense_gateup_workspace(big, 64, 64),
+                 lambda: B.moe_dense_gateup_backward_workspace(64, 64, big),
+                 lambda: B.moe_dense_linear(e(big, 64), w), lambda: B.moe_dense_linear_backward(e(big, 64), e(big, 64), w),
+                 lambda: B.moe_dense_gateup(e(64, big), e(64, big), e(64, big)),
+                 lambda: B.moe_dense_gateup_backward(e(big, 64), e(big, 64), w, w),
+                 lambda: B.moe_mxfp8_quantize(e(big, 64)), lambda: B.moe_mxfp8_quantize(e(64, big)),
+                 lambda: B.moe_mxfp8_dequant(e(big, 64, dt=u8), e(big, 2, dt=u8))):
+        with pytest.raises(B.MoeError, match="int32"):
+            call()
