@@ -459,6 +459,9 @@ struct DenseParts {
 };
 constexpr int kFinishRows = 16;   // rows per workgroup there, and per column-sum row of the launch
 constexpr int kSavedRows = 2;     // rows per workgroup of the saved pre-activations' gradients
+// Workgroups of 256 threads in a launch: a grid holds fewer than 2^32 threads.  The two kernels that the size limits let pass
+// it (few tokens of a very wide matrix, saved pre-activations of very many tokens) go out in pieces.
+constexpr int kMaxGrid = 1 << 23;
 
 // Sum the parts of the split tiles in order (the same order on every run), the terms of a row after each
 // other, and run the epilogue.  Workgroup `wg` of 256 threads takes kFinishRows rows of a tile; LANES threads a

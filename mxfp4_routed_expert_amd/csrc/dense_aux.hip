@@ -18,7 +18,6 @@ MOE_DEV Block block_of(int C) {
     const int n = col_blocks(C);
     return Block{(int)blockIdx.x / n, (int)blockIdx.x % n};
 }
-dim3 block_grid(int R, int rows, int C) { return dim3((unsigned)((R + rows - 1) / rows) * (unsigned)col_blocks(C)); }
 
 // Sum the parts of the split tiles.  Bound by the partial results, written just before and read from the last-level
 // cache: gate and up of 512 x 2368, six parts (60 MB), 10.7 us, 5.6 TB/s; five parts of 61 x 6144, two terms (16
@@ -51,8 +50,9 @@ __global__ __launch_bounds__(kFinishThreads) void dense_finish_kernel(const Dens
 
 // Gradients of the gated product from the saved bf16 pre-activations [2][R][C].  Two rows a workgroup, to fill
 // the CUs with few tokens: 61 x 2048 takes 4.6 us, most of it the launch.
-__global__ __launch_bounds__(kThreads) void gate_bwd_saved_kernel(const uint16_t *__restrict__ pre, int R, EpiGateBwd epi) {
-    const Block bl = block_of(epi.C);
+__global__ __launch_bounds__(kThreads) void gate_bwd_saved_kernel(const uint16_t *__restrict__ pre, int R, int rb0, EpiGateBwd epi) {
+    Block bl = block_of(epi.C);
+    bl.rb += rb0;
     const int c = bl.cb * kCols + threadIdx.x * 4;
     if (c >= epi.C) return;
     const int r = bl.rb * kSavedRows;
@@ -137,7 +137,9 @@ template moe_status dense_finish<EpiGateBwd>(const DenseParts &, const EpiGateBw
 template moe_status dense_finish<EpiStore>(const DenseParts &, const EpiStore &, hipStream_t);
 
 moe_status dense_gate_bwd_saved(const EpiGateBwd &e, const uint16_t *pre, int R, hipStream_t s) {
-    hipLaunchKernelGGL(gate_bwd_saved_kernel, block_grid(R, kSavedRows, e.C), dim3(kThreads), 0, s, pre, R, e);
+    const int rbs = (R + kSavedRows - 1) / kSavedRows, cbs = col_blocks(e.C), most = max(1, kMaxGrid / cbs);
+    for (int rb = 0; rb < rbs; rb += most)
+        hipLaunchKernelGGL(gate_bwd_saved_kernel, dim3((unsigned)(min(rbs - rb, most) * cbs)), dim3(kThreads), 0, s, pre, R, rb, e);
     return launch_check("gated gradients");
 }
 

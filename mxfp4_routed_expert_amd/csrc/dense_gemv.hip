@@ -41,13 +41,13 @@ MOE_DEV void butterfly(float (&v)[V]) {
 template <int MT, bool F32X, int G, class Epi>
 __global__ __launch_bounds__(64 * kWaves) void dense_gemv_kernel(const void *__restrict__ x, const uint16_t *__restrict__ w0,
                                                                  const uint16_t *__restrict__ w1, int T, int n, int K,
-                                                                 Epi epi) {
+                                                                 int c0, Epi epi) {
     constexpr int NM = Epi::kPair ? 2 : 1, ROWS = 4 * NM * G, V = ROWS * MT;
     static_assert(NM == 1 || G == 1, "a pair is two groups of rows");
     static_assert(V <= 64, "one value per lane after the butterfly");
     __shared__ float s_sum[kWaves][V];
     const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(wave_id());
-    const int c = blockIdx.x * (4 * G);
+    const int c = c0 + blockIdx.x * (4 * G);
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -134,8 +134,10 @@ moe_status launch(const void *x, const uint16_t *w0, const uint16_t *w1, int T, 
     constexpr int G = F32X ? 2 : 1;
     auto run = [&](auto mt, auto g) {
         constexpr int MT = decltype(mt)::value, GG = decltype(g)::value;
-        hipLaunchKernelGGL((dense_gemv_kernel<MT, F32X, GG, Epi>), dim3((unsigned)((n + 4 * GG - 1) / (4 * GG))),
-                           dim3(64 * kWaves), 0, s, x, w0, w1, T, n, K, e);
+        const int wgs = (n + 4 * GG - 1) / (4 * GG);
+        for (int b = 0; b < wgs; b += kMaxGrid)
+            hipLaunchKernelGGL((dense_gemv_kernel<MT, F32X, GG, Epi>), dim3((unsigned)min(wgs - b, kMaxGrid)), dim3(64 * kWaves), 0, s,
+                               x, w0, w1, T, n, K, b * 4 * GG, e);
     };
     using One = std::integral_constant<int, 1>;
     using Many = std::integral_constant<int, G>;

@@ -178,3 +178,25 @@ def test_weight_gradients_of_no_tokens_are_zeros(M, n, k, xt):
     out = [torch.full(s, math.nan, dtype=t, device="cuda") for s, t in (((f, k), bf16), ((f, k), bf16), ((f,), f32), ((f,), f32))]
     M.moe_dense_gateup_backward(dy[:, :f].contiguous(), x.to(bf16), w[:f], w[:f], want=("dw", "db"), out=(None, *out, None))
     assert all(not t.any() for t in out)
+
+
+def test_grids_of_more_threads_than_a_launch_holds(M):
+    # 2^26 columns at four a workgroup of 256 threads, and 2^25 rows at two: whole numbers, so results are exact
+    def ints(seed, lo, hi, *shape):
+        return torch.randint(lo, hi + 1, shape, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda", dtype=torch.int8).to(bf16)
+    n = 2 ** 26 + 24
+    w, wu, x = ints(1, -3, 3, n, 8), ints(2, -3, 3, n, 8), ints(3, 1, 2, 1, 8)
+    y = M.moe_dense_linear(x, w, out_dtype=f32)
+    z = (w * x).float().sum(1)
+    assert torch.equal(y[0], z)
+    del y
+    h = M.moe_dense_gateup(x, w, wu, act_fn="relu", out_dtype=f32)[0]
+    assert torch.equal(h[0], z.clamp(min=0) * (wu * x).float().sum(1))
+    del w, wu, h, z
+    T = 2 ** 25 + 6
+    pre, dh, wg, wu = ints(4, -1, 1, 2, T, 8), ints(5, -2, 2, T, 8), ints(6, -1, 1, 8, 8), ints(7, -1, 1, 8, 8)
+    dx, _, _, dbg, dbu, _ = M.moe_dense_gateup_backward(dh, None, wg, wu, act_fn="relu", pre=pre, want=("dx", "db"))
+    dg, du = dh.float() * pre[1].float() * (pre[0] > 0), dh.float() * pre[0].float().clamp(min=0)
+    assert torch.equal(dx.float(), dg @ wg.float() + du @ wu.float())
+    # (sums of 2^25 whole numbers of both signs stay below 2^24: exact in float32)
+    assert torch.equal(dbg.double(), dg.double().sum(0)) and torch.equal(dbu.double(), du.double().sum(0))
