@@ -200,3 +200,26 @@ def test_grids_of_more_threads_than_a_launch_holds(M):
     assert torch.equal(dx.float(), dg @ wg.float() + du @ wu.float())
     # (sums of 2^25 whole numbers of both signs stay below 2^24: exact in float32)
     assert torch.equal(dbg.double(), dg.double().sum(0)) and torch.equal(dbu.double(), du.double().sum(0))
+
+
+def test_short_workspaces_are_refused(M):
+    T, n, k = 64, 264, 136
+    x, w, dy = rnd(1, T, k, dtype=f32), rnd(2, n, k), rnd(3, T, n)
+    xb = x.to(bf16)
+    B = M.binding
+    calls = [(B.moe_dense_linear_workspace(T, n, k, x_dtype=f32, out_dtype=f32), lambda ws: (M.moe_dense_linear(x, w, ws=ws),)),
+             (B.moe_dense_linear_backward_workspace(T, n, k, "silu"), lambda ws: M.moe_dense_linear_backward(dy, xb, w, None, "silu", ws=ws)),
+             (B.moe_dense_gateup_workspace(T, 2376, 72), lambda ws: M.moe_dense_gateup(rnd(4, T, 2376), rnd(5, 72, 2376), rnd(6, 72, 2376), ws=ws)[:1]),
+             (B.moe_dense_gateup_backward_workspace(T, k, n), lambda ws: M.moe_dense_gateup_backward(dy, xb, w, w, ws=ws, want_h=True))]
+    for i, (need, call) in enumerate(calls):
+        assert need > 256, i
+        for have in (8, need - 1):
+            with pytest.raises(M.MoeError, match=f"workspace of {need} bytes needed, got {have}") as e:
+                call(torch.empty(have, dtype=torch.uint8, device="cuda"))
+            assert e.value.status == B.MOE_ERR_WORKSPACE
+        with pytest.raises(TypeError, match="ws"):
+            call(torch.empty(need, dtype=f32, device="cuda"))
+        with pytest.raises(ValueError, match="ws"):
+            call(torch.empty(need, dtype=torch.uint8))
+        for a, b in zip(call(torch.empty(need, dtype=torch.uint8, device="cuda")), call(None)):
+            assert torch.equal(a, b), i
