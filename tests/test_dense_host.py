@@ -244,3 +244,45 @@ def test_sizes_past_int32_are_refused(monkeypatch):
                  lambda: B.moe_mxfp8_dequant(e(big, 64, dt=u8), e(big, 2, dt=u8))):
         with pytest.raises(B.MoeError, match="int32"):
             call()
+
+
+def _forms(T, *sizes, gated=False, act=True, f32=False):
+    """(product, tile shape, how its sum is split) of a forward and a backward call, as csrc/dense.hip asks for them."""
+    def form(name, p):
+        tiles = p.tr * p.tc
+        return name, "LMSDWB"[p.cfg], "whole" if p.full == tiles else ("all tiles" if p.full == 0 else "last round")
+    few = T <= 64
+    if gated:
+        f, d = sizes
+        t = 2 if few else 1
+        return [form("gated", plan(FORWARD, T, f, d, pair=True)), form("gated dx", plan(INPUT_GRAD, T * t, d, f, 2, t)),
+                form("gated dw", plan(WEIGHT_GRAD, 2 * f, d, T, t))]
+    n, k = sizes
+    xs = 3 if f32 else 1                 # float32 rows: three terms, as rows or as segments
+    z = form("linear", plan(FORWARD, T * (xs if few else 1), n, k, 1 if few else xs, xs if few else 1))
+    t = 2 if act and few else 1          # terms of dz
+    return [z, form("linear dx", plan(INPUT_GRAD, T * t, k, n, 1, t)), form("linear dw", plan(WEIGHT_GRAD, n, k, T, (2 if f32 else 1) + t - 1))]
+
+
+def test_gpu_tests_reach_every_tile_shape_and_split():
+    import test_gpu_dense as G
+    import test_gpu_dense_edges as E
+    got = set()
+    for T, n, k in G.TILES:
+        got.update(_forms(T, n - 3, k)[:1] + _forms(T, n, k))
+    for T, k, n in G.TILES[1:]:
+        got.update(_forms(T, n - 1, k, act=False)[1:])
+    for T, n, k in G.GRAD_TILES:
+        got.update(_forms(T, n, k, act=False)[1:])
+    for T, n, k, xt in E.MORE_LINEAR:
+        got.update(_forms(T, n, k, f32=xt == torch.float32))
+    for T, f, d in G.PAIR_TILES + [(T, f, d) for T, d, f in G.TWO_PART_TILES] + E.MORE_GATED:
+        got.update(_forms(T, f, d, gated=True))
+    # forward products and input gradients take every shape but W, weight gradients L, B, M and W; the first two split no M
+    # tiles of a last round alone (none of 60000 drawn sizes did)
+    want = set()
+    for name in ("linear", "gated"):
+        for suffix, tiles in (("", "LBDMS"), (" dx", "LBDMS"), (" dw", "LBMW")):
+            want.update((name + suffix, t, s) for t in tiles for s in ("whole", "last round", "all tiles")
+                        if not (t == "M" and s == "last round" and suffix != " dw"))
+    assert want <= got, sorted(want - got)

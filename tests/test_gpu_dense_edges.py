@@ -223,3 +223,34 @@ def test_short_workspaces_are_refused(M):
             call(torch.empty(need, dtype=torch.uint8))
         for a, b in zip(call(torch.empty(need, dtype=torch.uint8, device="cuda")), call(None)):
             assert torch.equal(a, b), i
+
+
+# Sizes at which a product takes a tile shape in a form that those of test_gpu_dense.py do not reach (test_dense_host.py
+# asserts that the two together reach every one): (tokens, d_ff, d_model) of the gated block, (tokens, n, k) of a linear
+# layer with an activation and bf16 or float32 rows
+MORE_GATED = [(4725, 400, 3456), (73, 5672, 4072), (257, 6816, 5416), (564, 4688, 7904), (1298, 1608, 5432), (7873, 5992, 136),
+              (132, 7448, 808), (454, 64, 64), (7798, 5648, 272)]
+MORE_LINEAR = [(11, 64, 64, f32), (569, 7888, 3616, f32), (3511, 5704, 432, f32), (6035, 368, 5464, f32), (554, 6104, 7496, bf16)]
+
+
+def rnd_gpu(seed, *shape, std=1.0, dtype=bf16):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(*shape, generator=g, device="cuda") * std).to(dtype)
+
+
+@pytest.mark.parametrize("T,f,d", MORE_GATED)
+def test_more_gated_tiles(M, T, f, d):
+    x, wg, wu = rnd_gpu(1, T, d), rnd_gpu(2, f, d, std=d ** -0.5), rnd_gpu(3, f, d, std=d ** -0.5)
+    bg, bu, dh = rnd_gpu(4, f, dtype=f32), rnd_gpu(5, f, dtype=f32), rnd_gpu(6, T, f)
+    R.check(M.moe_dense_gateup(x, wg, wu, bg, bu, "silu")[0], R.gateup(x, wg, wu, bg, bu, "silu", bf16), "h")
+    got = M.moe_dense_gateup_backward(dh, x, wg, wu, bg, bu, "silu", want_h=True)
+    for name, g, r in zip(("dx", "dw_gate", "dw_up", "db_gate", "db_up", "h"), got, R.gateup_backward(dh, x, wg, wu, bg, bu, "silu")):
+        R.check(g, r, name)
+
+
+@pytest.mark.parametrize("T,n,k,xt", MORE_LINEAR)
+def test_more_linear_tiles(M, T, n, k, xt):
+    x, w, b, dy = rnd_gpu(1, T, k, dtype=xt), rnd_gpu(2, n, k, std=k ** -0.5), rnd_gpu(3, n, dtype=f32), rnd_gpu(4, T, n)
+    R.check(M.moe_dense_linear(x, w, b, "silu", out_dtype=f32), R.linear(x, w, b, "silu", None, f32), "y")
+    for name, g, r in zip(("dx", "dw", "dbias"), M.moe_dense_linear_backward(dy, x, w, b, "silu"), R.linear_backward(dy, x, w, b, "silu")):
+        R.check(g, r, name)
