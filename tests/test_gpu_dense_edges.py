@@ -254,3 +254,41 @@ def test_more_linear_tiles(M, T, n, k, xt):
     R.check(M.moe_dense_linear(x, w, b, "silu", out_dtype=f32), R.linear(x, w, b, "silu", None, f32), "y")
     for name, g, r in zip(("dx", "dw", "dbias"), M.moe_dense_linear_backward(dy, x, w, b, "silu"), R.linear_backward(dy, x, w, b, "silu")):
         R.check(g, r, name)
+
+
+def _slope(loss, args, i, v):
+    """d loss / d args[i] along v by central differences in float64, extrapolated from two steps."""
+    def d(eps):
+        up, dn = list(args), list(args)
+        up[i], dn[i] = args[i] + eps * v, args[i] - eps * v
+        return ((loss(up) - loss(dn)) / (2 * eps)).item()
+    step = 1e-3 / v.abs().max().item()
+    a, b = d(step), d(step / 2)
+    s = (4 * b - a) / 3
+    assert abs(b - a) <= 1e-4 * abs(s), "the step is too long"
+    return s
+
+
+@pytest.mark.parametrize("T", [7, 24, 90])
+@pytest.mark.parametrize("fn", ["silu", "gelu", "gelu_tanh"])
+def test_gradients_along_themselves_against_differences(M, fn, T):
+    # along a gradient g the loss rises by |g|^2: no signs cancel, so a factor in a derivative shows in full.  The error is at
+    # most the sum of the elements' bounds times |g|, 2^-8 of |g|^2 and less for bf16 results; the extrapolated
+    # differences leave 1e-4 squared
+    d, f = 64, 40
+    x, wg, wu = rnd(1, T, d), rnd(2, f, d, std=d ** -0.5), rnd(3, f, d, std=d ** -0.5)
+    bg, bu, dh = rnd(4, f, dtype=f32), rnd(5, f, dtype=f32), rnd(6, T, f)
+    args = [t.double() for t in (x, wg, wu, bg, bu)]
+    loss = lambda a: ((R.act(fn, a[0] @ a[1].t() + a[3])[0] * (a[0] @ a[2].t() + a[4])) * dh.double()).sum()
+    got = M.moe_dense_gateup_backward(dh, x, wg, wu, bg, bu, fn)
+    for i, (g, (_, tol)) in enumerate(zip(got[:5], R.gateup_backward(dh, x, wg, wu, bg, bu, fn)[:5])):
+        v = g.double()
+        num, ana = _slope(loss, args, i, v), (v * v).sum().item()
+        assert abs(num - ana) <= (tol * v.abs()).sum().item() + 1e-7 * ana, ("gated", i, num, ana)
+    args, loss = [t.double() for t in (x, wg, bg)], lambda a: (R.act(fn, a[0] @ a[1].t() + a[2])[0] * dh.double()).sum()
+    for xt in (bf16, f32):
+        got = M.moe_dense_linear_backward(dh, x.to(xt), wg, bg, fn, dx_dtype=f32)
+        for i, (g, (_, tol)) in enumerate(zip(got, R.linear_backward(dh, x.to(xt), wg, bg, fn, f32))):
+            v = g.double()
+            num, ana = _slope(loss, args, i, v), (v * v).sum().item()
+            assert abs(num - ana) <= (tol * v.abs()).sum().item() + 1e-7 * ana, ("linear", xt, i, num, ana)
