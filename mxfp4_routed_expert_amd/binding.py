@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import warnings
 from dataclasses import dataclass
 
 import torch
@@ -676,9 +677,15 @@ def _ws_for(ws, need, dev):
     return ws, ws.numel()
 
 
+def _outside_graph(who):
+    warnings.warn(f"{who}: an operand requires grad, but the result is not part of autograd's graph; its gradients come from "
+                  f"{who}_backward (under torch.no_grad() this is not said)", stacklevel=3)
+
+
 def moe_dense_linear(x, w, bias=None, act_fn="none", residual=None, out=None, out_dtype=None, ws=None):
     """y = act_fn(x w^T + bias) + residual.  x [T][kdim] bf16 or float32, w bf16 [n][kdim], bias float32 [n],
-    residual [T][n] of y's type; y [T][n] of out_dtype (x's type when None), bf16 or float32."""
+    residual [T][n] of y's type; y [T][n] of out_dtype (x's type when None), bf16 or float32.  Autograd does not see the
+    call (it warns of operands that require grad): moe_dense_linear_backward forms the gradients."""
     T, kdim = _matrix(x, "x")
     n = _matrix(w, "w")[0]
     dt = out.dtype if out is not None else (out_dtype or x.dtype)
@@ -687,6 +694,9 @@ def moe_dense_linear(x, w, bias=None, act_fn="none", residual=None, out=None, ou
     dev = x.device
     _operands(dev, (x, _one_of(x, DT), "x", None), (w, torch.bfloat16, "w", (n, kdim)), (bias, torch.float32, "bias", (n,)),
               (residual, dt, "residual", (T, n)), (out, dt, "out", (T, n)))
+    if (x.requires_grad or w.requires_grad or (bias is not None and bias.requires_grad)
+            or (residual is not None and residual.requires_grad)) and torch.is_grad_enabled():
+        _outside_graph("moe_dense_linear")
     d, need = _dense_plan("linear", T, n, kdim, _act_fn(act_fn), DT[x.dtype], DT[dt], 0)
     y = out if out is not None else torch.empty((T, n), dtype=dt, device=dev)
     ws, nws = _ws_for(ws, need, dev)
@@ -738,7 +748,8 @@ def moe_dense_gateup(x, w_gate, w_up, b_gate=None, b_up=None, act_fn="silu", out
                      pre=None, ws=None):
     """h = act_fn(x w_gate^T + b_gate) * (x w_up^T + b_up), both products in one kernel.  x bf16 [T][d_model], weights
     bf16 [d_ff][d_model], biases float32 [d_ff].  Returns (h [T][d_ff] of out_dtype (bf16 when None), the bf16
-    pre-activations [2][T][d_ff] for the backward call, or None)."""
+    pre-activations [2][T][d_ff] for the backward call, or None).  Autograd does not see the call (it warns of operands that
+    require grad): moe_dense_gateup_backward forms the gradients."""
     T, dm = _matrix(x, "x")
     f = _matrix(w_gate, "w_gate")[0]
     bf = torch.bfloat16
@@ -749,6 +760,9 @@ def moe_dense_gateup(x, w_gate, w_up, b_gate=None, b_up=None, act_fn="silu", out
     _operands(dev, (x, bf, "x", None), (w_gate, bf, "w_gate", (f, dm)), (w_up, bf, "w_up", (f, dm)),
               (b_gate, torch.float32, "b_gate", (f,)), (b_up, torch.float32, "b_up", (f,)), (out, dt, "out", (T, f)),
               (pre, bf, "pre", (2, T, f)))
+    if (x.requires_grad or w_gate.requires_grad or w_up.requires_grad or (b_gate is not None and b_gate.requires_grad)
+            or (b_up is not None and b_up.requires_grad)) and torch.is_grad_enabled():
+        _outside_graph("moe_dense_gateup")
     d, need = _dense_plan("gateup", T, dm, f, _act_fn(act_fn), 0, DT[dt])
     h = out if out is not None else torch.empty((T, f), dtype=dt, device=dev)
     if pre is None and want_pre:

@@ -286,3 +286,23 @@ def test_gpu_tests_reach_every_tile_shape_and_split():
             want.update((name + suffix, t, s) for t in tiles for s in ("whole", "last round", "all tiles")
                         if not (t == "M" and s == "last round" and suffix != " dw"))
     assert want <= got, sorted(want - got)
+
+
+def test_operands_that_require_grad_are_warned_of(monkeypatch):
+    import warnings
+    monkeypatch.setattr(B, "_operands", lambda *a: None)
+    monkeypatch.setattr(B, "_launch", lambda *a: None)
+    e = lambda *s, dt=torch.bfloat16: torch.empty(s, dtype=dt, device="meta")
+    linear = lambda x, w, b, r: B.moe_dense_linear(x, w, b, "silu", r)
+    gated = lambda x, w, b, r: B.moe_dense_gateup(x, w, w, b, b)
+    for call, who, n in ((linear, "moe_dense_linear_backward", 4), (gated, "moe_dense_gateup_backward", 3)):
+        for i in range(n):
+            t = [e(9, 64), e(32, 64), e(32, dt=torch.float32), e(9, 32)]
+            with warnings.catch_warnings():
+                warnings.simplefilter("error")
+                call(*t)
+                t[i].requires_grad_()
+                with torch.no_grad():
+                    call(*t)
+            with pytest.warns(UserWarning, match=who):
+                call(*t)
