@@ -468,10 +468,11 @@ size_t moe_dense_gateup_backward_workspace(const moe_gateup_desc *desc);
  * 32) to MXFP8: per 32-block scale byte X+127 with X = floor(log2 amax) - 8 clamped to [-127,127]
  * (byte 0 for an all-zero block, 0xFF and zero codes for a block holding NaN or Inf); codes =
  * nearest E4M3 of v/2^X, ties to even, saturating at 448, sign kept.  codes uint8 [rows][cols],
- * scales uint8 [rows][cols/32].  An activation kept this way for the backward pass takes 33/64 of
- * its bf16 bytes; both *_backward calls above read it directly.
- * moe_mxfp8_dequant -- E4M3(code) * 2^(scale-127) to bf16 (exact but for bf16's subnormals) or
- * float32.  values and codes 16-byte aligned.
+ * scales uint8 [rows][cols/32].  An activation kept this way between the passes takes 33/64 of
+ * its bf16 bytes; both *_backward calls above take it in place of x, and where they read x write it out
+ * as bf16 in their workspace first (a pass of its own, and 2 bytes a value while the call runs).
+ * moe_mxfp8_dequant -- E4M3(code) * 2^(scale-127) to bf16 (exact but for bf16's subnormals and values
+ * past its range, which moe_mxfp8_quantize does not write) or float32.  values and codes 16-byte aligned.
  * (The element and scale formats: rabbit README, architecture table, OCP MXFP4 and FP8 E4M3.)
  */
 moe_status moe_mxfp8_quantize(int32_t rows, int32_t cols, const void *x, int32_t x_dtype, uint8_t *codes,

@@ -239,8 +239,9 @@ class DenseFFN:
 
     forward(x, residual, train=True) keeps what backward(dy) needs: the input as it is (checkpoint="bf16": a reference,
     so it must not change until backward has run) or in 8 bits (checkpoint="mxfp8": a copy of 33/64 of its bytes, which
-    stands for x in every gradient).  The backward pass recomputes the gate and up products from it.  Buffers for T
-    tokens are allocated once; results of a call are overwritten by the next."""
+    stands for x in every gradient; the workspace has room for its bf16 form).  The backward pass recomputes the gate and up
+    products from it.  Buffers for T tokens and one workspace are allocated once: results of a call are overwritten by the
+    next, and calls must run in order (on one stream, or on streams that wait for each other).  Autograd does not see them."""
 
     def __init__(self, w_gate, w_up, w_down, T: int, act_fn: str = "silu", checkpoint: str = "bf16"):
         if checkpoint not in ("bf16", "mxfp8"):
