@@ -593,7 +593,15 @@ moe_status dense_split3(const float *x, uint16_t *planes, size_t n, hipStream_t 
 // Rows of C bf16 values -> rows of ld >= C, the tail zero.
 moe_status dense_pad_rows(const uint16_t *x, uint16_t *out, int R, int C, int ld, hipStream_t s);
 
-// Up to kGemvTokens tokens: one pass over the weights on the vector ALU (dense_gemv.hip).
+// Up to kGemvTokens tokens: one pass over the weights on the vector ALU (dense_gemv.hip).  Against the matrix cores,
+// which split the sum of so few tiles and need a launch more (float32 rows two, for their terms), us in graphs with weights
+// from HBM, forward products of 1 / 4 / 8 tokens:
+//   7168 x 2368, bf16 rows      7.7 /  8.8 / 12.3    13.4 / 14.2 / 14.3
+//   7168 x 2368, float32 rows   8.0 / 11.4 / 16.3    19.2 / 21.9 / 21.9
+//   2048 x 7168, bf16 rows      7.0 /  8.3 /  9.9    17.0 / 17.6 / 17.6
+//   2048 x 7168, float32 rows   7.0 / 10.2 / 18.7    24.3 / 30.1 / 30.1
+//   gate and up 2048 x 7168    10.9 / 12.2 / 14.6    16.6 / 16.5 / 16.5
+//   gate and up 2368 x 7168    13.5 / 15.2 / 18.9    17.2 / 17.1 / 17.2    (the one size where 8 tokens lose)
 constexpr int kGemvTokens = 8;
 moe_status dense_linear_gemv(const void *x, bool x_f32, const uint16_t *w, int T, int n, int k, const EpiLinear &e,
                              hipStream_t s);
