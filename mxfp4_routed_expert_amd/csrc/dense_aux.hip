@@ -20,8 +20,8 @@ MOE_DEV Block block_of(int C) {
 }
 
 // Sum the parts of the split tiles.  Bound by the partial results, written just before and read from the last-level
-// cache: gate and up of 512 x 2368, six parts (60 MB), 10.7 us, 5.6 TB/s; five parts of 61 x 6144, two terms (16
-// MB), 6.3 us, half of it the launch.  (Loads of four parts at a time measured the same.)
+// cache: gate and up of 512 x 2368, three parts (29 MB), 6.4 us, 4.5 TB/s with the launch; five parts of 61 x 6144, two
+// terms (16 MB), 6.3 us as a launch of its own, half of it the launch.  (Loads of four parts at a time measured the same.)
 template <int LANES, class Epi>
 __global__ __launch_bounds__(kFinishThreads) void dense_finish_kernel(const DenseParts q, Epi epi) {
     constexpr int kStep = kFinishThreads / LANES;

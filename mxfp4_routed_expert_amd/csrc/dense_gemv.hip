@@ -1,7 +1,7 @@
 // Dense products of a few tokens (T <= 8): one pass over the weights on the vector ALU.
 //
-// Bound by the weight bytes (one token, 2048 x 7168: 6.4 us, 4.6 TB/s; gate and up of 2368 x 7168: 13.5 us,
-// 5.0 TB/s).  A workgroup of four waves owns four consecutive output columns (four gate and four up rows
+// Bound by the weight bytes (one token, in graphs, weights from HBM: 2048 x 7168 7.0 us, 4.2 TB/s; gate and up of 2368 x
+// 7168 14.6 us, 4.7 TB/s; 6.0 and 13.7 us with weights partly in the last-level cache).  A workgroup of four waves owns four consecutive output columns (four gate and four up rows
 // for the pair, eight columns with several float32 rows); its waves take every fourth 512-value piece of the
 // sum, a lane 8 consecutive values of each row, so every load is a whole 1 KiB line run of one
 // row and a wave keeps 8 or more of them in flight.  The tokens' values of a piece are read once
