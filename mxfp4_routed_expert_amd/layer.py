@@ -241,7 +241,8 @@ class DenseFFN:
     so it must not change until backward has run) or in 8 bits (checkpoint="mxfp8": a copy of 33/64 of its bytes, which
     stands for x in every gradient; the workspace has room for its bf16 form).  The backward pass recomputes the gate and up
     products from it.  Buffers for T tokens and one workspace are allocated once: results of a call are overwritten by the
-    next, and calls must run in order (on one stream, or on streams that wait for each other).  Autograd does not see them."""
+    next, and calls must run in order (on one stream, or on streams that wait for each other); x, residual and dy may be
+    the block's own last results.  Autograd does not see the calls."""
 
     def __init__(self, w_gate, w_up, w_down, T: int, act_fn: str = "silu", checkpoint: str = "bf16"):
         if checkpoint not in ("bf16", "mxfp8"):
@@ -268,11 +269,19 @@ class DenseFFN:
                    B.moe_dense_gateup_backward_workspace(T, d, f, act_fn, mx))
         self.ws = B._workspace(need, dev)
 
+    def _mine(self, t):
+        """Whether t is (part of) a result of an earlier call."""
+        return t.untyped_storage().data_ptr() in (self.y.untyped_storage().data_ptr(), self.dx.untyped_storage().data_ptr())
+
     def forward(self, x, residual=None, train: bool = False):
+        # the input is kept before anything is written: it may be this block's own last result
+        saved = self.saved
+        if train:
+            self.saved = None                  # (its buffers are written now)
+            saved = B.moe_mxfp8_quantize(x, out=self.x_saved) if self.x_saved is not None else (x.clone() if self._mine(x) else x, None)
         B.moe_dense_gateup(x, self.wg, self.wu, act_fn=self.act_fn, out=self.h, ws=self.ws)
         B.moe_dense_linear(self.h, self.wd, residual=residual, out=self.y, ws=self.ws)
-        if train:
-            self.saved = B.moe_mxfp8_quantize(x, out=self.x_saved) if self.x_saved is not None else (x, None)
+        self.saved = saved
         return self.y
 
     def backward(self, dy):
@@ -280,6 +289,8 @@ class DenseFFN:
         if self.saved is None:
             raise B.MoeError(B.MOE_ERR_INVALID_ARG, "DenseFFN.backward: no forward(..., train=True) before it")
         x, xs = self.saved
+        if self._mine(dy):                     # dx is written before dw_down reads dy
+            dy = dy.clone()
         B.moe_dense_linear_backward(dy, None, self.wd, want=("dx",), out=(self.dh, None, None), ws=self.ws)
         B.moe_dense_gateup_backward(self.dh, x, self.wg, self.wu, act_fn=self.act_fn, x_scales=xs, want=("dx", "dw"),
                                     want_h=True, out=(self.dx, self.dwg, self.dwu, None, None, self.h), ws=self.ws)

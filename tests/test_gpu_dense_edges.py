@@ -292,3 +292,26 @@ def test_gradients_along_themselves_against_differences(M, fn, T):
             v = g.double()
             num, ana = _slope(loss, args, i, v), (v * v).sum().item()
             assert abs(num - ana) <= (tol * v.abs()).sum().item() + 1e-7 * ana, ("linear", xt, i, num, ana)
+
+
+@pytest.mark.parametrize("checkpoint", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("T", [24, 100])
+def test_block_called_on_its_own_results(M, checkpoint, T):
+    # one block several times: its output is its next input, and its input's gradient the next pass's dy
+    d, f = 96, 136
+    w = rnd(1, f, d, std=d ** -0.5), rnd(2, f, d, std=d ** -0.5), rnd(3, d, f, std=f ** -0.5)
+    a, b = (M.DenseFFN(*w, T, checkpoint=checkpoint) for _ in range(2))
+    y, ref, dy = rnd(4, T, d), rnd(4, T, d), rnd(5, T, d)
+    for step in range(3):
+        y, ref = a.forward(y, y, train=True), b.forward(ref.clone(), ref.clone(), train=True)
+        assert torch.equal(y, ref), step
+        want = b.backward(dy.clone())
+        for i, (g, r) in enumerate(zip(a.backward(dy), want)):
+            assert torch.equal(g, r), (step, i)
+        # (the gradient with respect to the input, in the block's own buffer, is what comes next)
+        dy = a.dx
+    assert a.forward(y, train=True) is y
+    keep = rnd(4, T, d)
+    first = b.forward(keep, train=True).clone()
+    want = [t.clone() for t in b.backward(first)]
+    assert all(torch.equal(g, r) for g, r in zip((a.forward(keep, train=True), a.backward(a.y))[1], want))
