@@ -315,3 +315,38 @@ def test_block_called_on_its_own_results(M, checkpoint, T):
     first = b.forward(keep, train=True).clone()
     want = [t.clone() for t in b.backward(first)]
     assert all(torch.equal(g, r) for g, r in zip((a.forward(keep, train=True), a.backward(a.y))[1], want))
+
+
+def test_offsets_past_two_gib_within_a_tile(M):
+    # operands near the size limit: a tile's rows, or the rows of one step, lie up to 4 GiB apart.  One value a sum, so
+    # results are exact
+    def pattern(rows, cols):
+        t = torch.empty(rows, cols, dtype=bf16, device="cuda")
+        a = torch.arange(cols, device="cuda", dtype=torch.int32)
+        for r in range(rows):
+            t[r] = (a + 5 * r) % 251 - 125
+        return t
+    k = 2 ** 23
+    x, w = torch.zeros(250, k, dtype=bf16, device="cuda"), pattern(40, k)
+    at = [(0, 3), (127, k - 1), (128, 2 ** 22), (200, 0), (249, k - 1)]
+    for r, c in at:
+        x[r, c] = 2
+    y = M.moe_dense_linear(x, w, out_dtype=f32)
+    for r, c in at:
+        assert torch.equal(y[r], 2 * w[:, c].float()), (r, c)
+        y[r] = 0
+    assert not y.any()
+    del x, y, w
+    n, k = 64, 2 ** 25 - 8
+    w, dy = pattern(n, k), torch.zeros(3, n, dtype=bf16, device="cuda")
+    dy[0, 63], dy[1, 0], dy[2, 40] = 1, 2, -1
+    dx = M.moe_dense_linear_backward(dy, None, w, want=("dx",))[0]
+    assert torch.equal(dx[0], w[63]) and torch.equal(dx[1], 2 * w[0]) and torch.equal(dx[2], -w[40])
+    del w, dy, dx
+    T, n = 72, 29826000
+    dy, x = pattern(T, n), torch.zeros(T, 8, dtype=bf16, device="cuda")
+    for j in range(8):
+        x[9 * j, j] = 1
+    dw = M.moe_dense_linear_backward(dy, x, torch.empty(n, 8, dtype=bf16, device="cuda"), want=("dw",))[1]
+    for j in range(8):
+        assert torch.equal(dw[:, j], dy[9 * j]), j
