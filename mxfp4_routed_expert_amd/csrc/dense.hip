@@ -143,9 +143,11 @@ moe_status check_linear(const char *who, const moe_linear_desc *d, bool backward
         MOE_REQUIRE(d->x_dtype == MOE_DT_BF16 || d->x_dtype == MOE_DT_F32, "%s: unknown x_dtype %d", who, d->x_dtype);
         MOE_REQUIRE(d->y_dtype == MOE_DT_BF16 || d->y_dtype == MOE_DT_F32, "%s: unknown y_dtype %d", who, d->y_dtype);
     }
-    // (the terms of few rows form one operand, whose tile offsets are 32-bit bytes: three of x, two of dz)
-    const int64_t x_rows = (int64_t)d->T * (d->T <= kTermTokens && d->x_dtype == MOE_DT_F32 ? 3 : 1);
-    const int64_t z_rows = (int64_t)d->T * (d->T <= kTermTokens && backward ? 2 : 1);
+    // (where few rows are kept as several terms these form one operand, whose tile offsets are 32-bit bytes: three of x for a
+    // product on the matrix cores, two of dz behind an activation)
+    const bool few = d->T <= kTermTokens, act = d->fn != MOE_FN_NONE;
+    const int64_t x_rows = (int64_t)d->T * (few && d->x_dtype == MOE_DT_F32 && (backward ? act : d->T > kGemvTokens) ? 3 : 1);
+    const int64_t z_rows = (int64_t)d->T * (few && backward && act ? 2 : 1);
     MOE_REQUIRE(fits31(z_rows, (int64_t)d->n + 8) && fits31(d->n, d->kdim) && fits31(x_rows, d->kdim), "%s: sizes overflow int32",
                 who);
     return MOE_OK;

@@ -306,3 +306,16 @@ def test_operands_that_require_grad_are_warned_of(monkeypatch):
                     call(*t)
             with pytest.warns(UserWarning, match=who):
                 call(*t)
+
+
+def test_size_limit_counts_terms_only_where_they_are_kept():
+    # without an activation dz is dy itself, one term, and x enters dw as segments; up to 8 tokens a forward pass multiplies float32
+    T, n, k = 64, (2 ** 31 - 1) // 64 // 8 * 8 - 16, (2 ** 31 - 1) // 64 // 8 * 8
+    assert lib.moe_dense_linear_backward_workspace(lin(T=T, n=n, kdim=8)) > 0
+    assert lib.moe_dense_linear_backward_workspace(lin(T=T, n=8, kdim=k, x_dtype=1)) > 0
+    few = lin(T=8, n=1, kdim=(2 ** 31 - 1) // 8 // 8 * 8, x_dtype=1)
+    refused(lib.moe_dense_linear(few, P, P, None, None, ODD, None, 0, None), B.MOE_ERR_INVALID_ARG, "aligned")
+    for kw in (dict(T=T, n=n, kdim=8, fn=1), dict(T=T, n=8, kdim=k, x_dtype=1, fn=1)):
+        assert lib.moe_dense_linear_backward_workspace(lin(**kw)) == 0
+        assert "overflow" in B.last_error()
+    assert lib.moe_dense_linear_workspace(lin(T=T, n=8, kdim=k, x_dtype=1)) == 0 and "overflow" in B.last_error()

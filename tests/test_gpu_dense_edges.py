@@ -343,10 +343,11 @@ def test_offsets_past_two_gib_within_a_tile(M):
     dx = M.moe_dense_linear_backward(dy, None, w, want=("dx",))[0]
     assert torch.equal(dx[0], w[63]) and torch.equal(dx[1], 2 * w[0]) and torch.equal(dx[2], -w[40])
     del w, dy, dx
-    T, n = 72, 29826000
-    dy, x = pattern(T, n), torch.zeros(T, 8, dtype=bf16, device="cuda")
-    for j in range(8):
-        x[9 * j, j] = 1
-    dw = M.moe_dense_linear_backward(dy, x, torch.empty(n, 8, dtype=bf16, device="cuda"), want=("dw",))[1]
-    for j in range(8):
-        assert torch.equal(dw[:, j], dy[9 * j]), j
+    for T, n in ((72, 29826000), (64, 2 ** 25 - 16)):
+        dy, x = pattern(T, n), torch.zeros(T, 8, dtype=bf16, device="cuda")
+        for j in range(8):
+            x[7 * j, j] = 1
+        dw = M.moe_dense_linear_backward(dy, x, torch.empty(n, 8, dtype=bf16, device="cuda"), want=("dw",))[1]
+        for j in range(8):
+            assert torch.equal(dw[:, j], dy[7 * j]), (T, j)
+        del dy, x, dw
