@@ -386,7 +386,8 @@ moe_status moe_mx_quantize(int32_t rows, int32_t cols, const void *x, int32_t x_
  * outputs apart from inputs and from each other unless a call says otherwise; kdim, d_model and
  * d_ff multiples of 8.  A NaN or infinity reaches the outputs whose sums it takes part in, and no
  * others (an infinity may arrive as NaN where it meets a value kept as several terms, some of them
- * 0, and silu and gelu of minus infinity and their derivatives at either infinity are NaN).  Results depend on the arguments alone: the same call gives the same bits (sums have a fixed
+ * 0, and silu and gelu of minus infinity and their derivatives at either infinity are NaN).
+ * Results depend on the arguments alone: the same call gives the same bits (sums have a fixed
  * order; no atomics).  The workspace is 16-byte aligned; calls that may run at the same time (other
  * streams, other captured graphs) need one each.
  *

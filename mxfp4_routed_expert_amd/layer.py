@@ -269,16 +269,16 @@ class DenseFFN:
                    B.moe_dense_gateup_backward_workspace(T, d, f, act_fn, mx))
         self.ws = B._workspace(need, dev)
 
-    def _mine(self, t):
-        """Whether t is (part of) a result of an earlier call."""
-        return t.untyped_storage().data_ptr() in (self.y.untyped_storage().data_ptr(), self.dx.untyped_storage().data_ptr())
+    @staticmethod
+    def _within(t, *buffers):
+        return isinstance(t, torch.Tensor) and any(t.untyped_storage().data_ptr() == b.untyped_storage().data_ptr() for b in buffers)
 
     def forward(self, x, residual=None, train: bool = False):
         # the input is kept before anything is written: it may be this block's own last result
         saved = self.saved
         if train:
             self.saved = None                  # (its buffers are written now)
-            saved = B.moe_mxfp8_quantize(x, out=self.x_saved) if self.x_saved is not None else (x.clone() if self._mine(x) else x, None)
+            saved = B.moe_mxfp8_quantize(x, out=self.x_saved) if self.x_saved is not None else (x.clone() if self._within(x, self.y, self.dx) else x, None)
         B.moe_dense_gateup(x, self.wg, self.wu, act_fn=self.act_fn, out=self.h, ws=self.ws)
         B.moe_dense_linear(self.h, self.wd, residual=residual, out=self.y, ws=self.ws)
         self.saved = saved
@@ -289,7 +289,7 @@ class DenseFFN:
         if self.saved is None:
             raise B.MoeError(B.MOE_ERR_INVALID_ARG, "DenseFFN.backward: no forward(..., train=True) before it")
         x, xs = self.saved
-        if self._mine(dy):                     # dx is written before dw_down reads dy
+        if self._within(dy, self.dx):          # dx is written before dw_down reads dy
             dy = dy.clone()
         B.moe_dense_linear_backward(dy, None, self.wd, want=("dx",), out=(self.dh, None, None), ws=self.ws)
         B.moe_dense_gateup_backward(self.dh, x, self.wg, self.wu, act_fn=self.act_fn, x_scales=xs, want=("dx", "dw"),
