@@ -53,7 +53,8 @@ MOE_DEV float rcp(float v) { return __builtin_amdgcn_rcpf(v); }
 // (least-squares fit of erfc(x) exp(x^2) / 2 with equalised relative error, 1.3e-7 over x >= 0).  Phi is that for
 // negative z and 1 minus it otherwise: no cancellation on either side, and the value keeps its relative accuracy
 // as far out as it is a normal number (z about -13).  A result rounded to bf16 takes it too: bf16 has float32's exponents, so
-// the tail is stored, and a gated h is scaled by u first.
+// the tail is stored, and a gated h is scaled by u first (4093 x 7168 x 2048 with bias: 107 us, 103 with a polynomial logit
+// that holds to z = -5; a fit of six terms for bf16, 2^-18 of the value, measured the same 107).
 MOE_DEV float phi_of(float z, float E) {
     const float t = rcp(fmaf(0.28284271f, fabsf(z), 1.0f));
     float q = 0.025137422606348991f;

@@ -250,7 +250,7 @@ def _forms(T, *sizes, gated=False, act=True, f32=False):
     """(product, tile shape, how its sum is split) of a forward and a backward call, as csrc/dense.hip asks for them."""
     def form(name, p):
         tiles = p.tr * p.tc
-        return name, "LMSDWB"[p.cfg], "whole" if p.full == tiles else ("all tiles" if p.full == 0 else "last round")
+        return name, "LMSDWB"[p.cfg], "whole" if p.full == tiles else ("all tiles" if p.full == 0 else "tail")
     few = T <= 64
     if gated:
         f, d = sizes
@@ -279,12 +279,12 @@ def test_gpu_tests_reach_every_tile_shape_and_split():
     for T, f, d in G.PAIR_TILES + [(T, f, d) for T, d, f in G.TWO_PART_TILES] + E.MORE_GATED:
         got.update(_forms(T, f, d, gated=True))
     # forward products and input gradients take every shape but W, weight gradients L, B, M and W; the first two split no M
-    # tiles of a last round alone (none of 60000 drawn sizes did)
+    # tail tiles alone (none of 60000 drawn sizes did)
     want = set()
     for name in ("linear", "gated"):
         for suffix, tiles in (("", "LBDMS"), (" dx", "LBDMS"), (" dw", "LBMW")):
-            want.update((name + suffix, t, s) for t in tiles for s in ("whole", "last round", "all tiles")
-                        if not (t == "M" and s == "last round" and suffix != " dw"))
+            want.update((name + suffix, t, s) for t in tiles for s in ("whole", "tail", "all tiles")
+                        if not (t == "M" and s == "tail" and suffix != " dw"))
     assert want <= got, sorted(want - got)
 
 
