@@ -1004,8 +1004,18 @@ def _gate_kind(gate, T, d):
     raise ValueError(f"gate has shape {tuple(gate.shape)}, expected {(T, 1)} (a token's) or {(1, d)} (a channel's)")
 
 
-@functools.lru_cache(maxsize=4096)
+def _constant(v):
+    """A number (or what holds one, such as a tensor of one element) as the C side's float, its value at this call; -0 as 0."""
+    return _f32(v).value + 0.0
+
+
 def _norm_desc(T, d, zt, yt, kind, eps, residual_scale, dropout):
+    # (values, not objects: a tensor is the same key after its value has changed)
+    return _norm_plan(T, d, zt, yt, kind, _constant(eps), _constant(residual_scale), _constant(dropout))
+
+
+@functools.lru_cache(maxsize=4096)
+def _norm_plan(T, d, zt, yt, kind, eps, residual_scale, dropout):
     """(descriptor, workspace bytes of the backward call): a function of sizes, types and constants alone."""
     _int32(T, d)
     n = ctypes.byref(BlockNormDesc(T, d, zt, yt, kind, eps, residual_scale, dropout))
@@ -1023,7 +1033,9 @@ def moe_block_norm(z, w_after=None, gate=None, residual=None, w_before=None, res
     (one a channel); residual [T][d] of y's type; rng: int64 or uint64 [2] device tensor (seed, offset), needed with dropout and read when
     the call runs.  Returns (y, u, u_codes, u_scales): y of y_dtype (residual's type, or bf16); u bf16, and its FP8 form
     (moe_fp8_quantize's rows) with want_codes, when w_before is given; None for what is not wanted.  want_u: None means yes.  out: the
-    four results' tensors (y may be the residual).  The norm before a block alone: z, w_before, want_y=False."""
+    four results' tensors (y may be the residual).  The norm before a block alone: z, w_before, want_y=False.
+    residual_scale, dropout and eps are numbers; a tensor of one element counts with its value at the call, and a captured graph keeps
+    that value."""
     T, d = _matrix(z, "z")
     yt = residual.dtype if isinstance(residual, torch.Tensor) else (
         out[0].dtype if out is not None and out[0] is not None else (y_dtype or torch.bfloat16))
