@@ -183,6 +183,13 @@ def _need(t, dtype, name, shape=None):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
+def _room(t, dtype, name, n):
+    """An optional tensor that a call reads or writes n elements of: of dtype, contiguous, no shorter, in device memory."""
+    if t is not None and isinstance(t, torch.Tensor) and t.dtype == dtype and t.numel() < n:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, room for {n} values is needed")
+    _need(t, dtype, name)
+
+
 def _workspace(nbytes: int, device):
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=device)
 
@@ -372,6 +379,16 @@ def moe_expert_gateup_workspace(w: ExpertWeights, act, T, k):
     return lib.moe_expert_gateup_workspace(ctypes.byref(w.c_struct()), ACT[act], T, k)
 
 
+def _expert_rows(w, act, R, expert_offsets, h, h_codes, h_scales):
+    """Room for R rows of h in the forms that `act` reads and writes (the codes' width depends on it)."""
+    _room(expert_offsets, torch.int32, "expert_offsets", w.num_experts + 1)
+    _room(h, torch.float32, "h", R * w.d_ff)
+    if act != "float":
+        fp8 = act == "fp8"
+        _room(h_codes, torch.uint8, "h_codes", R * (w.d_ff if fp8 else w.d_ff // 2))
+        _room(h_scales, torch.uint8, "h_scales", R * (w.d_ff // (128 if fp8 else 32)))
+
+
 def moe_expert_gateup(w: ExpertWeights, x, act="float", k=1, expert_offsets=None, sorted_pairs=None,
                       want_h=True, out=None, ws=None):
     """Returns (h float32 [R][d_ff] or None, h_codes or None, h_scales or None): codes [R][d_ff/2] with scales [R][d_ff/32]
@@ -393,6 +410,9 @@ def moe_expert_gateup(w: ExpertWeights, x, act="float", k=1, expert_offsets=None
         elif act == "fp8":
             hq = torch.empty((R, w.d_ff), dtype=torch.uint8, device=dev)
             hs = torch.empty((R, w.d_ff // 128), dtype=torch.uint8, device=dev)
+    _expert_rows(w, act, R, expert_offsets, h, hq, hs)
+    _room(sorted_pairs, torch.int32, "sorted_pairs", R)
+    _need(ws, None, "ws")
     if ws is None:
         ws = _workspace(lib.moe_expert_gateup_workspace(ctypes.byref(c), ACT[act], T, kk), dev)
     check(lib.moe_expert_gateup(ctypes.byref(c), ACT[act], T, kk, _ptr(x), DT[x.dtype], _ptr(expert_offsets),
@@ -407,6 +427,8 @@ def moe_expert_down(w: ExpertWeights, T, act="float", k=1, expert_offsets=None, 
     R = T * kk
     dev = (h if h is not None else h_codes).device
     y = out if out is not None else torch.empty((R, w.d_model), dtype=torch.float32, device=dev)
+    _expert_rows(w, act, R, expert_offsets, h if act == "float" else None, h_codes, h_scales)
+    _room(y, torch.float32, "y_rows", R * w.d_model)
     check(lib.moe_expert_down(ctypes.byref(c), ACT[act], T, kk, _ptr(h), _ptr(h_codes), _ptr(h_scales),
                               _ptr(expert_offsets), _ptr(y), _stream()))
     return y

@@ -31,3 +31,78 @@ def test_norm_constants_of_every_kind():
     for bad in ("0.5", None, torch.tensor([1.0, 2.0])):
         with pytest.raises((TypeError, ValueError)):
             B._norm_desc(4, 64, 0, 0, 0, 1e-6, bad, 0.0)
+
+
+# ------------------------------------------------------------------ the experts' buffers
+
+def _experts(fmt, E=2, H=256, I=128):
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    if fmt == "fp8b128":
+        s = lambda *n: torch.ones(n)
+        return B.ExpertWeights(fmt, H, I, u8(E, I, H), s(E, 1, 2), u8(E, I, H), s(E, 1, 2), u8(E, H, I), s(E, 2, 1))
+    return B.ExpertWeights(fmt, H, I, u8(E, I, H // 2), u8(E, I, H // 32), u8(E, I, H // 2), u8(E, I, H // 32), u8(E, H, I // 2), u8(E, H, I // 32))
+
+
+@pytest.mark.parametrize("act,fmt,codes,scales", [("fp8", "fp8b128", 128, 1), ("mxfp4", "mxfp4", 64, 4), ("float", "mxfp4", 64, 4)])
+def test_experts_refuse_short_buffers(monkeypatch, act, fmt, codes, scales):
+    """Buffers of another mode, or a row short, are refused before a kernel could run past their end."""
+    class Reached(Exception):
+        pass
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_workspace"):
+                return lambda *a: 16
+            raise Reached(name)
+    monkeypatch.setattr(B, "lib", Lib())
+    # (host tensors: all but the place of a tensor is checked here)
+    need = B._need
+
+    def anywhere(t, dtype, name, shape=None):
+        try:
+            need(t, dtype, name, shape)
+        except ValueError as e:
+            if "device memory" not in str(e):
+                raise
+            if dtype is not None and t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}")
+    monkeypatch.setattr(B, "_need", anywhere)
+    w, T, k = _experts(fmt), 3, 2
+    R, H, I = T * k, w.d_model, w.d_ff
+    x = torch.zeros(T, H, dtype=torch.bfloat16)
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8)
+    offs, sp = torch.zeros(3, dtype=torch.int32), torch.zeros(R, dtype=torch.int32)
+    h, hq, hs, y = torch.zeros(R, I), u8(R, codes), u8(R, scales), torch.zeros(R, H)
+    gateup = lambda h=h, hq=hq, hs=hs, offs=offs, sp=sp: B.moe_expert_gateup(w, x, act, k, offs, sp, out=(h, hq, hs))
+    down = lambda h=h, hq=hq, hs=hs, offs=offs, y=y: B.moe_expert_down(w, T, act, k, offs, h, hq, hs, out=y)
+    for call in (gateup, down):
+        with pytest.raises(Reached):
+            call()
+        with pytest.raises(ValueError, match="expert_offsets"):
+            call(offs=offs[:2])
+        with pytest.raises(TypeError, match="expert_offsets"):
+            call(offs=offs.long())
+    if act == "float":
+        for call in (gateup, down):
+            with pytest.raises(ValueError, match="h has shape"):
+                call(h=h[:R - 1])
+    else:
+        for call in (gateup, down):
+            for short in (dict(hq=hq[:R - 1]), dict(hs=hs[:R - 1]), dict(hq=u8(R, codes // 2))):
+                with pytest.raises(ValueError, match="h_codes has shape|h_scales has shape"):
+                    call(**short)
+            with pytest.raises(TypeError, match="h_codes"):
+                call(hq=hq.float())
+        with pytest.raises(Reached):
+            gateup(h=None)
+    with pytest.raises(ValueError, match="h has shape"):
+        gateup(h=h[:R - 1])
+    with pytest.raises(ValueError, match="sorted_pairs"):
+        gateup(sp=sp[:R - 1])
+    with pytest.raises(ValueError, match="y_rows"):
+        down(y=y[:R - 1])
+    with pytest.raises(TypeError, match="y_rows"):
+        down(y=y.bfloat16())
+    # buffers of more rows are taken, as before
+    with pytest.raises(Reached):
+        gateup(h=torch.zeros(R + 1, I), hq=u8(R + 1, codes), hs=u8(R + 1, scales))
