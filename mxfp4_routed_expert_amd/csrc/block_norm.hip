@@ -5,6 +5,8 @@
 // m the dropout factor (0 or 1 / (1 - p)).  Gradients, with t = dL/dy in all:
 //   t = dy + r(y) (w_b du) - y r(y)^3 mean(w_b du y),          dresidual = rs t,   dw_before = sum_T du y r(y)
 //   a = gate m t,  dz = r(z) (w_a a) - z r(z)^3 mean(w_a a z),  dw_after = sum_T a z r(z),  dgate = sum m t n.
+// r^3 leaves float32 for rows that do not (2^50: 2^-150), so each r is multiplied with a factor of its own size: the gradients are
+// r (w a - z (r (r mean))).
 // Both sums over a row that dz needs are known before t is (those of z, y and du) or follow from one more, so a row
 // is in registers from its one read to its one write.
 //
@@ -401,7 +403,7 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxThreads) void block_norm_backward_
         const float rz = a.w_after ? rsqrtf(fmaf(s[0], inv_d, a.eps)) : 1.0f;
         if (a.w_before) {
             const float ry = rsqrtf(fmaf(s[1], inv_d, a.eps));
-            const float k = ry * ry * ry * (s[2] * inv_d);
+            const float k = ry * (ry * (s[2] * inv_d));
 #pragma unroll
             for (int c = 0; c < NC; ++c) {
                 f8 w;
@@ -409,7 +411,7 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxThreads) void block_norm_backward_
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     sb[c][i] = fmaf(g[c][i], y[c][i] * ry, sb[c][i]);
-                    tt[c][i] += fmaf(-y[c][i], k, ry * (g[c][i] * w[i]));
+                    tt[c][i] += ry * fmaf(-y[c][i], k, g[c][i] * w[i]);
                 }
             }
         }
@@ -435,12 +437,12 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxThreads) void block_norm_backward_
         }
         if (a.w_after || a.dgate_row) row_sums<WAVE, 1>(q, lds, turn);
         __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(rz * q[0]), row_of(a.dgate_row, t, a.T, 4), tid == 0 ? 0 : kNowhere, 0, 0);
-        const float k = a.w_after ? rz * rz * rz * (gt * q[0] * inv_d) : 0.0f;
+        const float k = a.w_after ? rz * (rz * (gt * q[0] * inv_d)) : 0.0f;
         const Row zr = row_of(a.dz, t, a.T, zb);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) tt[c][i] = fmaf(-z[c][i], k, rz * gt * tt[c][i]);
+            for (int i = 0; i < 8; ++i) tt[c][i] = rz * fmaf(-z[c][i], k, gt * tt[c][i]);
             store8<ZF>(zr, tid + c * lanes, tt[c]);
         }
     }

@@ -21,3 +21,74 @@ def test_constants_that_change_between_calls(M):
             assert torch.equal(y, M.moe_block_norm(z, residual=res, residual_scale=v, y_dtype=F32)[0])
             dr = M.moe_block_norm_backward(z, dy=dy, residual_scale=s, y_dtype=F32, want=("dresidual",))[1]
             assert torch.equal(dr, v * dy)
+
+
+# ------------------------------------------------------------------ gradients of given rows
+
+NAMES = ("dz", "dresidual", "dw_after", "dgate", "dw_before")
+
+
+def gradients(M, z, w_after=None, gate=None, y=None, w_before=None, du=None, dy=None, rs=1.0, eps=1e-6, p=0.0, rng=None):
+    yt = next(t.dtype for t in (dy, y) if t is not None)
+    got = M.moe_block_norm_backward(on(z), w_after=on(w_after), gate=on(gate), y=on(y), w_before=on(w_before), du=on(du), dy=on(dy),
+                                    residual_scale=rs, dropout=p, rng=on(rng), eps=eps, y_dtype=yt)
+    return dict(zip(NAMES, (d64(t) for t in got)))
+
+
+def expected(z, w_after, gate, y, w_before, du, dy, rs, eps, m, zt, yt):
+    """(reference, tolerance) of dz and dresidual in 64 bits: each of a value's terms within 4 REL (two means, two roots and
+    products), a float32 product that leaves its normal range off by 2^-149 more, and the result's rounding."""
+    one = torch.ones(1, 1, dtype=torch.float64)
+    t, tm = torch.zeros_like(z), torch.zeros_like(z)
+    if dy is not None:
+        t, tm = dy.clone(), dy.abs()
+    if w_before is not None:
+        ry, v = R.rms(y, eps), du * w_before
+        t = t + ry * (v - y * ry * ry * (v * y).mean(1, keepdim=True))
+        tm = tm + ry * (v.abs() + y.abs() * ry * ry * (v * y).abs().mean(1, keepdim=True))
+    a, am = (one if gate is None else gate) * m * t, (one if gate is None else gate.abs()) * m * tm
+    if w_after is not None:
+        rz, v, vm = R.rms(z, eps), a * w_after, am * w_after.abs()
+        dz, dzm = rz * (v - z * rz * rz * (v * z).mean(1, keepdim=True)), rz * (vm + z.abs() * rz * rz * (vm * z.abs()).mean(1, keepdim=True))
+    else:
+        dz, dzm = a, am
+    tol = lambda ref, mag, dt: (4 * REL * mag + half(dt) * ref.abs()) * (1 + 2.0 ** -8) + 2.0 ** -140
+    return dict(dz=(dz, tol(dz, dzm, zt)), dresidual=(rs * t, tol(rs * t, rs * tm, yt)))
+
+
+def close(got, want):
+    for name, (ref, tol) in want.items():
+        err = (got[name] - ref).abs()
+        assert (err <= tol).all(), f"{name}: {(err / tol).max():.3g} of the tolerance"
+
+
+@pytest.mark.parametrize("zt,yt", [(F32, F32), (BF, BF)])
+@pytest.mark.parametrize("d", [64, 520, 1040, 8208])
+def test_gradients_of_large_and_small_rows(M, d, zt, yt):
+    """Rows of 2^-60 to 2^56: the sum of squares stays in float32, r^3 does not.  The part along the row is as large as the one that
+    it is taken from: a gradient along the row itself cancels."""
+    T = 10
+    scale = torch.tensor([2.0 ** e for e in (0, 42, 46, 48, 50, 52, 56, -20, -45, -60)])[:, None]
+    z, y = (rnd(1, T, d) * scale).to(zt), (rnd(2, T, d) * scale.flip(0)).to(yt)
+    wa, wb, g = rnd(3, d).abs() + 0.3, rnd(4, d).abs() + 0.3, rnd(5, T, 1)
+    dy, du = rnd(6, T, d, dt=yt), rnd(7, T, d, dt=BF)
+    eps = 1e-6
+    args = dict(w_after=wa, gate=g, y=y, w_before=wb, du=du, dy=dy)
+    want = expected(d64(z), d64(wa), d64(g), d64(y), d64(wb), d64(du), d64(dy), 0.5, eps, 1.0, zt, yt)
+    close(gradients(M, z, rs=0.5, eps=eps, **args), want)
+    along = (z.float() / scale / wa).to(yt)                    # w_a dy is the row itself
+    want = expected(d64(z), d64(wa), None, None, None, None, d64(along), 1.0, eps, 1.0, zt, yt)
+    close(gradients(M, z, w_after=wa, dy=along, eps=eps), want)
+
+
+@pytest.mark.parametrize("eps", [1e-12, 1e-26, 1e-30, 1e-37])
+def test_gradients_of_zero_rows_with_small_eps(M, eps):
+    """r is 1 / sqrt(eps) there and its cube leaves float32; the mean that it multiplies is 0."""
+    T, d = 3, 264
+    z, y = torch.zeros(T, d), torch.zeros(T, d)
+    z[1], y[2] = rnd(1, d), rnd(2, d)
+    wa, wb, dy, du = rnd(3, d), rnd(4, d), rnd(5, T, d), rnd(6, T, d, dt=BF)
+    dy, du = dy * 2.0 ** -20, du * 2.0 ** -20
+    want = expected(d64(z), d64(wa), None, d64(y), d64(wb), d64(du), d64(dy), 1.0, eps, 1.0, F32, F32)
+    assert all(torch.isfinite(ref).all() for ref, _ in want.values())
+    close(gradients(M, z, w_after=wa, y=y, w_before=wb, du=du, dy=dy, eps=eps), want)
