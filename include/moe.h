@@ -570,7 +570,8 @@ size_t moe_fp8_linear_workspace(const moe_fp8_linear_desc *desc);
  *   dresidual = residual_scale t [T][d] of y_dtype;  dz [T][d] of z_dtype;  dw_after, dw_before float32 [d];
  *   dgate float32 [T] or [d], as gate.  Any of them may be NULL, not all.
  *   z, w_after, gate, rng, w_before as in the forward call, y its result (needed with w_before, as is du, bf16); dy of y_dtype.
- *   z may be NULL when neither dgate nor dw_after nor, with w_after, dz is asked for.
+ *   z may be NULL when neither dgate nor dw_after nor, with w_after, dz is asked for; without w_after dz does not depend on it.  A
+ *   dropped element's m n is 0 in dgate and dw_after, as in the forward call.
  *   The column sums have a fixed order (no atomics).  With T == 0 they are written as zeros, and nothing need be asked for.
  */
 enum { MOE_GATE_NONE = 0, MOE_GATE_TOKEN = 1, MOE_GATE_CHANNEL = 2 };

@@ -5,8 +5,8 @@
 // m the dropout factor (0 or 1 / (1 - p)).  Gradients, with t = dL/dy in all:
 //   t = dy + r(y) (w_b du) - y r(y)^3 mean(w_b du y),          dresidual = rs t,   dw_before = sum_T du y r(y)
 //   a = gate m t,  dz = r(z) (w_a a) - z r(z)^3 mean(w_a a z),  dw_after = sum_T a z r(z),  dgate = sum m t n.
-// r^3 leaves float32 for rows that do not (2^50: 2^-150), so each r is multiplied with a factor of its own size: the gradients are
-// r (w a - z (r (r mean))).
+// r^3 leaves float32 for rows that do not (2^50: 2^-150), so each r is multiplied with a factor of its own size: dz = r (w_a a -
+// z r mean(w_a a z r)), y's the same.  A dropped element's m n is 0 in every sum, also where n is NaN or infinite.
 // Both sums over a row that dz needs are known before t is (those of z, y and du) or follow from one more, so a row
 // is in registers from its one read to its one write.
 //
@@ -182,14 +182,15 @@ MOE_DEV Philox philox_of(const NormArgs &a) {
     }
     return g;
 }
-// v times the dropout factors of a chunk
-MOE_DEV void drop8(const NormArgs &a, const Philox &g, uint64_t chunk, f8 &v) {
+// v times the dropout factors of a chunk; n: 0 where an element is dropped, whatever it held
+MOE_DEV void drop8(const NormArgs &a, const Philox &g, uint64_t chunk, f8 &v, f8 *n = nullptr) {
     uint32_t c[4];
     g.bits(chunk, c);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t half = (i & 1) ? c[i >> 1] >> 16 : c[i >> 1] & 0xffffu;
         v[i] = half >= a.cut ? v[i] * a.keep_scale : 0.0f;
+        if (n) (*n)[i] = half >= a.cut ? (*n)[i] : 0.0f;
     }
 }
 
@@ -425,24 +426,28 @@ __global__ __launch_bounds__(WAVE ? 256 : kMaxThreads) void block_norm_backward_
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[i] = a.rs * tt[c][i];
             store8<YF>(rr, ch, o);
-            if (a.cut) drop8(a, rng, (uint64_t)t * (unsigned)a.chunks + (unsigned)ch, tt[c]);
+            f8 n;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) n[i] = z[c][i] * rz;
+            if (a.cut) drop8(a, rng, (uint64_t)t * (unsigned)a.chunks + (unsigned)ch, tt[c], &n);
             f8 w;
             wc.get(c, ch, w);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                sa[c][i] = fmaf(gt * tt[c][i], z[c][i] * rz, sa[c][i]);
+                sa[c][i] = fmaf(gt * tt[c][i], n[i], sa[c][i]);
                 tt[c][i] *= w[i];
-                q[0] = fmaf(tt[c][i], z[c][i], q[0]);
+                q[0] = fmaf(tt[c][i], n[i], q[0]);
             }
         }
         if (a.w_after || a.dgate_row) row_sums<WAVE, 1>(q, lds, turn);
-        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(rz * q[0]), row_of(a.dgate_row, t, a.T, 4), tid == 0 ? 0 : kNowhere, 0, 0);
-        const float k = a.w_after ? rz * (rz * (gt * q[0] * inv_d)) : 0.0f;
+        __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(q[0]), row_of(a.dgate_row, t, a.T, 4), tid == 0 ? 0 : kNowhere, 0, 0);
+        const float mean = gt * q[0] * inv_d;
         const Row zr = row_of(a.dz, t, a.T, zb);
 #pragma unroll
         for (int c = 0; c < NC; ++c) {
+            // (no norm after: dz does not depend on z, which may be infinite)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) tt[c][i] = rz * fmaf(-z[c][i], k, gt * tt[c][i]);
+            for (int i = 0; i < 8; ++i) tt[c][i] = a.w_after ? rz * fmaf(-(z[c][i] * rz), mean, gt * tt[c][i]) : gt * tt[c][i];
             store8<ZF>(zr, tid + c * lanes, tt[c]);
         }
     }

@@ -92,3 +92,56 @@ def test_gradients_of_zero_rows_with_small_eps(M, eps):
     want = expected(d64(z), d64(wa), None, d64(y), d64(wb), d64(du), d64(dy), 1.0, eps, 1.0, F32, F32)
     assert all(torch.isfinite(ref).all() for ref, _ in want.values())
     close(gradients(M, z, w_after=wa, y=y, w_before=wb, du=du, dy=dy, eps=eps), want)
+
+
+# ------------------------------------------------------------------ values that take no part
+
+@pytest.mark.parametrize("zt", [F32, BF])
+@pytest.mark.parametrize("gate", ["none", "token", "channel"])
+def test_without_a_norm_after_dz_does_not_depend_on_z(M, zt, gate):
+    """dz = gate m t: infinite and NaN z change nothing, nor does a z that is not given."""
+    T, d, p = 6, 520, 0.25
+    s = make(T, d, zt, F32, False, True, gate, p, seed=3)
+    z = s["z"].clone()
+    z[1, 5], z[2, 7], z[3, 300], z[4] = float("inf"), float("nan"), float("-inf"), 3.0e38
+    y, du, dy = rnd(11, T, d), rnd(12, T, d, dt=BF), rnd(13, T, d)
+    kw = dict(gate=on(s["gate"]), y=on(y), w_before=on(s["w_before"]), du=on(du), dy=on(dy), dropout=p, rng=on(s["rng"]), want=("dz", "dresidual"))
+    ref = M.moe_block_norm_backward(on(s["z"]), **kw)
+    for got in (M.moe_block_norm_backward(on(z), **kw), M.moe_block_norm_backward(None, z_dtype=zt, **kw)):
+        assert torch.isfinite(ref[0]).all() and torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
+
+
+@pytest.mark.parametrize("after,bad", [(False, float("nan")), (False, float("inf")), (True, float("inf"))])
+@pytest.mark.parametrize("d", [64, 520, 1040, 8208])
+def test_dropped_elements_take_no_part_in_the_gates_and_weights_gradients(M, d, after, bad):
+    """m n is 0 there whatever n is (an infinite z makes n NaN: inf * 0): dgate and dw_after are those of a 0 in its place."""
+    T, p = 5, 0.5
+    s = make(T, d, F32, F32, after, False, "token", p, seed=9)
+    z, zero = s["z"].clone(), s["z"].clone()
+    hit = []
+    for t in (1, 3):
+        c = int((s["m"][t] == 0).nonzero()[t])
+        z[t, c], zero[t, c] = bad, 0.0
+        hit.append((t, c))
+    dy, ch = rnd(14, T, d), rnd(15, 1, d)
+    for gate in (s["gate"], ch):
+        kw = dict(w_after=on(s["w_after"]), gate=on(gate), dy=on(dy), dropout=p, rng=on(s["rng"]), y_dtype=F32, want=("dw_after", "dgate") if after else ("dgate",))
+        got, plain = M.moe_block_norm_backward(on(z), **kw), M.moe_block_norm_backward(on(zero), **kw)
+        for i in (2, 3):
+            if got[i] is None:
+                continue
+            assert torch.isfinite(got[i]).all()
+            if not after:                                     # (with a norm an infinite z makes r and its row's other n 0)
+                assert torch.equal(got[i], plain[i])
+        if after:
+            # rows with an infinity: r = 0, so n is 0 but where z is infinite, and m n is 0 there too
+            keep = torch.ones(T, 1, dtype=torch.float64)
+            keep[[t for t, _ in hit]] = 0.0
+            zr, wa, a = d64(zero), d64(s["w_after"]), s["m"] * d64(dy)
+            n0 = keep * zr * R.rms(zr, 1e-6)
+            col = 4 * REL + (T + 16) * 2.0 ** -24
+            g = d64(gate)
+            want_w, mag_w = (a * g * n0).sum(0), (a * g * n0).abs().sum(0)
+            assert ((d64(got[2]) - want_w).abs() <= col * mag_w + 1e-30).all()
+            n1, dim = a * n0 * wa, 1 if gate is s["gate"] else 0
+            assert ((d64(got[3]) - n1.sum(dim, keepdim=True)).abs() <= (col + d * 2.0 ** -24) * n1.abs().sum(dim, keepdim=True) + 1e-30).all()
