@@ -725,9 +725,9 @@ def _ws_for(ws, need, dev):
     return ws, ws.numel()
 
 
-def _outside_graph(who):
+def _outside_graph(who, backward=None):
     warnings.warn(f"{who}: an operand requires grad, but the result is not part of autograd's graph; its gradients come from "
-                  f"{who}_backward (under torch.no_grad() this is not said)", stacklevel=3)
+                  f"{backward or who + '_backward'} (under torch.no_grad() this is not said)", stacklevel=3)
 
 
 def moe_dense_linear(x, w, bias=None, act_fn="none", residual=None, out=None, out_dtype=None, ws=None):
@@ -895,6 +895,9 @@ def _blocks(n):
     return (n + 127) // 128
 
 
+_FP8_GRADIENTS = "moe_fp8_linear on the transposed codes (FP8Linear.backward)"
+
+
 def _fp8_pairs(out, wanted, shapes, types, dev):
     """The code and scale tensors of a quantiser: `out`'s (checked), new ones, or None where not wanted."""
     names = ("codes", "scales", "codes_t", "scales_t")
@@ -908,7 +911,7 @@ def moe_fp8_quantize(x, rows=True, cols=False, out=None):
     """x (bf16 or float32 [T][d], d a multiple of 8) as E4M3 codes with an E8M0 scale per 128 values.  Returns (codes [T][d],
     scales [T][ceil(d/128)], codes_t [d][ld], scales_t [d][ceil(T/128)]), uint8: the first two (blocks along the row) with
     `rows`, the last two (the transpose, blocks along the column, ld = T rounded up to 16) with `cols`, else None.  out: the
-    four tensors."""
+    four tensors.  Autograd does not see the call (it warns of an x that requires grad)."""
     T, d = _matrix(x, "x")
     _int32(T, d)
     if not (rows or cols):
@@ -916,6 +919,8 @@ def moe_fp8_quantize(x, rows=True, cols=False, out=None):
     dev, u8 = x.device, torch.uint8
     ld = (T + 15) // 16 * 16
     _operands(dev, (x, _one_of(x, DT), "x", None))
+    if x.requires_grad and torch.is_grad_enabled():
+        _outside_graph("moe_fp8_quantize", _FP8_GRADIENTS)
     c, s, ct, st = _fp8_pairs(out, (rows, rows, cols, cols), ((T, d), (T, _blocks(d)), (d, ld), (d, _blocks(T))), (u8,) * 4, dev)
     _launch(dev, lib.moe_fp8_quantize, T, d, _at(x), DT[x.dtype], _at(c), _at(s), _at(ct), _at(st))
     return c, s, ct, st
@@ -925,7 +930,7 @@ def moe_fp8_quantize_weight(w, scale_dtype=torch.float32, codes=True, transpose=
     """A weight (bf16 or float32 [n][kdim], kdim a multiple of 16) as E4M3 codes with a scale (a power of two; float32, or uint8:
     E8M0) per 128 x 128 block.  Returns (codes [n][kdim], scales [ceil(n/128)][ceil(kdim/128)], codes_t [kdim][ld], scales_t
     [ceil(kdim/128)][ceil(n/128)]); the last two, the same codes transposed (ld = n rounded up to 16), with `transpose`, the
-    first two with `codes`, else None.  out: the four tensors."""
+    first two with `codes`, else None.  out: the four tensors.  Autograd does not see the call (it warns of a w that requires grad)."""
     n, k = _matrix(w, "w")
     _int32(n, k)
     if not (codes or transpose):
@@ -935,6 +940,8 @@ def moe_fp8_quantize_weight(w, scale_dtype=torch.float32, codes=True, transpose=
     dev, u8, sd = w.device, torch.uint8, scale_dtype
     ld = (n + 15) // 16 * 16
     _operands(dev, (w, _one_of(w, DT), "w", None))
+    if w.requires_grad and torch.is_grad_enabled():
+        _outside_graph("moe_fp8_quantize_weight", _FP8_GRADIENTS)
     c, s, ct, st = _fp8_pairs(out, (codes, codes, transpose, transpose),
                               ((n, k), (_blocks(n), _blocks(k)), (k, ld), (_blocks(k), _blocks(n))), (u8, sd, u8, sd), dev)
     _launch(dev, lib.moe_fp8_quantize_weight, n, k, _at(w), DT[w.dtype], FP8_SCALE_F32 if sd is torch.float32 else FP8_SCALE_E8M0,
@@ -979,7 +986,7 @@ def moe_fp8_linear(x, w, w_scales, x_scales=None, residual=None, out=None, out_d
     """y = x w^T + residual of block-128 FP8 operands.  x [T][kdim]: bf16 or float32 (quantised by the call), or uint8 codes with
     x_scales uint8 [T][ceil(kdim/128)] (moe_fp8_quantize).  w uint8 codes [n][kdim]; w_scales: float32 or uint8 (E8M0)
     [ceil(n/128)][ceil(kdim/128)], or uint8 [n][ceil(kdim/128)] (a row's own).  residual [T][n] of y's type (may be `out`);
-    y [T][n] of out_dtype (bf16 when None), bf16 or float32.  Autograd does not see the call."""
+    y [T][n] of out_dtype (bf16 when None), bf16 or float32.  Autograd does not see the call (it warns of operands that require grad)."""
     T, kdim = _matrix(x, "x")
     n = _matrix(w, "w")[0]
     dt = out.dtype if out is not None else (out_dtype or torch.bfloat16)
@@ -1000,7 +1007,7 @@ def moe_fp8_linear(x, w, w_scales, x_scales=None, residual=None, out=None, out_d
                   (w_scales, _one_of(w_scales, (torch.float32, u8)), "w_scales", sshape), (x_scales, u8, "x_scales", (T, kb)),
                   (residual, dt, "residual", (T, n)), (out, dt, "out", (T, n)))
     if torch.is_grad_enabled() and (x.requires_grad or (residual is not None and residual.requires_grad)):
-        _outside_graph("moe_fp8_linear")
+        _outside_graph("moe_fp8_linear", _FP8_GRADIENTS)
     d, need = _fp8_plan(T, n, kdim, _x_dtype(x.dtype), DT[dt], kind)
     y = out if out is not None else torch.empty((T, n), dtype=dt, device=dev)
     ws, nws = _ws_for(ws, need, dev)

@@ -310,7 +310,8 @@ class FP8Linear:
     transpose for the weight gradient (train=False: keeps nothing); backward(dy) gives dx and dw, bf16 (dw float32 with
     dw_dtype; dw_accumulate adds to the last dw, zeros at first, for a batch in pieces).  x and dy are bf16 or float32 [T][.].
     Buffers for T tokens and one workspace are allocated once: results of a call are overwritten by the next, and calls must
-    run in order (on one stream, or on streams that wait for each other).  Autograd does not see the calls."""
+    run in order (on one stream, or on streams that wait for each other).  Autograd does not see the calls (they warn of a weight,
+    x or residual that requires grad)."""
 
     def __init__(self, w, T: int, dw_dtype=torch.bfloat16):
         n, k = w.shape
