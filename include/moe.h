@@ -223,7 +223,8 @@ size_t moe_expert_ffn_workspace(const moe_expert_weights *w, int32_t act, int32_
  *   MOE_ACT_FP8:   h_codes uint8 [R][d_ff] (16-byte aligned) and h_scales uint8 [R][d_ff/128] required (h quantised
  *                  as by moe_fp8_quantize); h (float32, before quantisation, 16-byte aligned) optional.
  *                  R / 256 + num_experts at most 65535.
- *   ws: moe_expert_gateup_workspace(w, act, T, k) bytes (k ignored in the identity form).
+ *   ws: moe_expert_gateup_workspace(w, act, T, k) bytes (k ignored in the identity form); as moe_expert_ffn's, a workspace for T
+ *       and k serves fewer of either.
  * moe_expert_down writes y_rows[r] = down_e . h[r] from h (FLOAT) or h_codes/h_scales (MXFP4, FP8).
  */
 moe_status moe_expert_gateup(const moe_expert_weights *w, int32_t act, int32_t T, int32_t k,

@@ -105,14 +105,15 @@ FfnWs ffn_ws_layout(const moe_expert_weights *w, int act, int T, int R, bool wit
         l.xq = take((size_t)T * w->d_model / 2);
         l.xs = take((size_t)T * w->d_model / 32);
     }
-    if (act == MOE_ACT_FP8) {                // (h exists in float32 for few rows only)
+    if (act == MOE_ACT_FP8) {                // (h is held in float32 for few rows only)
         l.xq = take((size_t)T * w->d_model);
         l.xs = take((size_t)T * (w->d_model / kFp8Block));
         if (with_hq) {
             l.hq = take((size_t)R * w->d_ff);
             l.hs = take((size_t)R * (w->d_ff / kFp8Block));
         }
-        if (R <= kFp8FewRows) l.h = (float *)take((size_t)R * w->d_ff * sizeof(float));
+        // (also of more rows, where it is not used: a workspace for T and k is then one for fewer of either)
+        l.h = (float *)take((size_t)(R < kFp8FewRows ? R : kFp8FewRows) * w->d_ff * sizeof(float));
         l.bytes = off;
         return l;
     }

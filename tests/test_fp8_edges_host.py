@@ -106,3 +106,32 @@ def test_experts_refuse_short_buffers(monkeypatch, act, fmt, codes, scales):
     # buffers of more rows are taken, as before
     with pytest.raises(Reached):
         gateup(h=torch.zeros(R + 1, I), hq=u8(R + 1, codes), hs=u8(R + 1, scales))
+
+
+# ------------------------------------------------------------------ workspaces
+
+@pytest.mark.parametrize("query", ["moe_expert_gateup_workspace", "moe_expert_ffn_workspace"])
+@pytest.mark.parametrize("act", [1, 2])
+@pytest.mark.parametrize("E,H,I", [(1, 256, 128), (1, 128, 1024), (64, 1024, 512)])
+def test_expert_workspaces_grow_with_tokens_and_k(query, act, E, H, I):
+    """A workspace for T tokens and top k serves fewer of either (the identity form ignores k: any k's serves it)."""
+    P = 0x10000
+    w = B.ExpertWeightsC(1 if act == 2 else 0, E, H, I, P, P, P, P, P, P)
+    f = lambda T, k: getattr(lib, query)(ctypes.byref(w), act, T, k)
+    for k in (1, 2, 8):
+        sizes = [f(T, k) for T in (1, 2, 4, 5, 15, 16, 17, 31, 32, 33, 64, 100, 1000)]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+    for T in (1, 3, 5, 16, 32, 33):
+        sizes = [f(T, k) for k in (1, 2, 3, 8, 32)]
+        assert sizes == sorted(sizes)
+
+
+def test_identity_form_takes_a_workspace_of_any_k():
+    P = ctypes.c_void_p(0x10000)
+    w = B.ExpertWeightsC(1, 1, 128, 1024, *[P.value] * 6)
+    T, k = 8, 8
+    need = lib.moe_expert_gateup_workspace(ctypes.byref(w), 2, T, k)
+    # (the alignment of x is checked first and the workspace last: neither reaches the device)
+    call = lambda n: lib.moe_expert_gateup(ctypes.byref(w), 2, T, k, P, 0, None, None, None, P, P, P, n, None)
+    assert need >= lib.moe_expert_gateup_workspace(ctypes.byref(w), 2, T, 1)
+    assert call(lib.moe_expert_gateup_workspace(ctypes.byref(w), 2, T, 1) - 1) == B.MOE_ERR_WORKSPACE
