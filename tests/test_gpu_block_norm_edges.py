@@ -145,3 +145,43 @@ def test_dropped_elements_take_no_part_in_the_gates_and_weights_gradients(M, d, 
             assert ((d64(got[2]) - want_w).abs() <= col * mag_w + 1e-30).all()
             n1, dim = a * n0 * wa, 1 if gate is s["gate"] else 0
             assert ((d64(got[3]) - n1.sum(dim, keepdim=True)).abs() <= (col + d * 2.0 ** -24) * n1.abs().sum(dim, keepdim=True) + 1e-30).all()
+
+
+# ------------------------------------------------------------------ rows walked one behind the other
+
+# More rows than a forward launch has workgroups (512) or, up to 1024 values a row, waves (2048): the next row is in flight while one is
+# worked on, and the two buffers of its sums take turns.
+@pytest.mark.parametrize("T,d", [(2049, 64), (4100, 8), (2500, 1000), (513, 1032), (1100, 7168), (1025, 8208), (520, 16384)])
+@pytest.mark.parametrize("zt,yt,after,before,gate,p", [(BF, BF, True, True, "channel", 0.25), (F32, F32, True, True, "token", 0.0),
+                                                      (BF, F32, False, True, "none", 0.1), (F32, BF, True, False, "token", 0.0)])
+def test_forward_many_rows(M, T, d, zt, yt, after, before, gate, p):
+    s = make(T, d, zt, yt, after, before, gate, p, seed=60)
+    rs, eps = 0.75, 1e-5
+    io = on(s["residual"]).clone()                             # the residual is the result
+    y, u, c, sc = M.moe_block_norm(on(s["z"]), w_after=on(s["w_after"]), gate=on(s["gate"]), residual=io, w_before=on(s["w_before"]),
+                                   residual_scale=rs, dropout=p, rng=on(s["rng"]), eps=eps, want_codes=before, out=(io, None, None, None))
+    assert y is io
+    branch = R.block_norm(d64(s["z"]), d64(s["w_after"]), d64(s["gate"]), None, 1.0, s["m"], eps)
+    ref = rs * d64(s["residual"]) + branch
+    tol = REL * branch.abs() + 2.0 ** -23 * (ref.abs() + (rs * d64(s["residual"])).abs())
+    tol = tol * (1 + half(yt)) + half(yt) * ref.abs() + 1e-30
+    err = (d64(y) - ref).abs()
+    assert (err <= tol).all(), f"row {int((err > tol).any(1).nonzero()[0])}"
+    apart = M.moe_block_norm(on(s["z"]), w_after=on(s["w_after"]), gate=on(s["gate"]), residual=on(s["residual"]), w_before=on(s["w_before"]),
+                             residual_scale=rs, dropout=p, rng=on(s["rng"]), eps=eps)
+    assert torch.equal(apart[0], y)
+    if not before:
+        return
+    assert torch.equal(apart[1], u)
+    yk = d64(y)
+    uref = yk * R.rms(yk, eps) * d64(s["w_before"])
+    assert ((d64(u) - uref).abs() <= (REL + 2.0 ** -8) * uref.abs() + 1e-30).all()
+    qc, qs = M.moe_fp8_quantize(u)[:2]
+    assert torch.equal(c, qc) and torch.equal(sc, qs)
+
+
+@pytest.mark.parametrize("T,d", [(1025, 64), (1025, 1000), (257, 1032), (300, 8208)])
+def test_backward_first_rows_that_are_walked(M, T, d):
+    """A row more than a backward launch has waves (1024) or workgroups (256)."""
+    check_backward(M, T, d, BF, F32, True, True, "token", 0.1, True)
+    check_backward(M, T, d, F32, BF, True, False, "channel", 0.0, True)
