@@ -85,6 +85,12 @@ struct Fp8Product {
     uint8_t *hq, *hs;             // h as codes [R][N] and scales [R][N/128]
 };
 
+// What moe_fp8_linear does with its sizes: rows of a tile and parts of the sum; no rows: the weights are streamed.
+struct Fp8Plan {
+    int bt, split;
+};
+Fp8Plan fp8_linear_plan(const moe_fp8_linear_desc *d);
+
 moe_status fp8_product_launch(const Fp8Product &p, bool pair, hipStream_t s, const char *what);
 // Few rows: the weights stream once (fp8_stream.hip).  fp8_stream_launch: rows of experts (float32 weight scales), the gated pair
 // or float32 results of multiples of 4 columns; fp8_rows16_launch: up to 64 rows of one matrix, or rows of experts (float32

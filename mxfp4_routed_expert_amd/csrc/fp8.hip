@@ -14,9 +14,7 @@ namespace {
 // of a last, short round are halved or quartered.  Parts are written, and read by a second launch, at 6.5 TB/s.  Measured
 // (us; [rows, parts]): 333 x 2368 x 7168 [128,4] 25.6, [128,8] 24.3, [256,3] 28.6, [64,3] 30.6; 1021 x 6144 x 2048 [128,1] 22.8,
 // [256,1] 23.8, [192,1] 28.9, [128,2] 37.1; 4096 x 7168 x 7168 [256,1] 204, [192,1] 232, [128,1] 290.
-struct Plan {
-    int bt, split;
-};
+using Plan = Fp8Plan;
 Plan plan_of(int R, int N, int Kb) {
     constexpr int G = 256;
     const int NT = (N + 255) / 256;
@@ -59,7 +57,7 @@ Layout layout_of(const moe_fp8_linear_desc *d) {
     Layout l;
     if (direct_x(d)) return l;                            // (quantised on the way, no parts)
     const int Kb = fp8_blocks(d->kdim);
-    l.plan = few_rows(d) ? Plan{64, 1} : plan_of(d->T, d->n, Kb);
+    l.plan = fp8_linear_plan(d);
     size_t off = 0;
     auto take = [&](size_t b) {
         const size_t at = off;
@@ -89,6 +87,10 @@ moe_status check_desc(const moe_fp8_linear_desc *d, const char *who) {
 }
 
 }  // namespace
+
+Fp8Plan fp8_linear_plan(const moe_fp8_linear_desc *d) {
+    return few_rows(d) ? Plan{0, 1} : plan_of(d->T, d->n, fp8_blocks(d->kdim));
+}
 }  // namespace moe
 
 using namespace moe;

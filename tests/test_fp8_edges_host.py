@@ -135,3 +135,19 @@ def test_identity_form_takes_a_workspace_of_any_k():
     call = lambda n: lib.moe_expert_gateup(ctypes.byref(w), 2, T, k, P, 0, None, None, None, P, P, P, n, None)
     assert need >= lib.moe_expert_gateup_workspace(ctypes.byref(w), 2, T, 1)
     assert call(lib.moe_expert_gateup_workspace(ctypes.byref(w), 2, T, 1) - 1) == B.MOE_ERR_WORKSPACE
+
+
+# ------------------------------------------------------------------ the GPU tests' sizes
+
+def test_tiles_cover_the_forms():
+    """Every size of tile with whole and split sums, a second window of each kind of scale, and a second unit."""
+    from test_gpu_fp8_edges import EVERY, TILES, linear_forms, plan
+    seen = {}
+    for T, n, k, want, kinds in TILES:
+        for kind in kinds:
+            got = linear_forms(T, n, k, kind)
+            assert want <= got, (T, n, k, kind, plan(T, n, k), want - got)
+            seen.setdefault(kind, set()).update(got)
+    for kind in EVERY:
+        for tt in (1, 2, 3, 4):
+            assert {(tt, w) for w in ("one", "split", "window", "again")} <= seen[kind] | {(1, "split")}, (kind, tt, seen[kind])

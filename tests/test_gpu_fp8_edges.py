@@ -1,6 +1,7 @@
 """Block-128 FP8 operators at their edges (GPU): what autograd sees, workspaces, tiles of every size, windows of scales."""
 from __future__ import annotations
 
+import ctypes
 import warnings
 
 import pytest
@@ -29,3 +30,257 @@ def test_operands_that_require_grad_are_warned_of(M):
         warnings.simplefilter("error")
         layer.forward(x, r)
         layer.backward(r)
+
+
+# ------------------------------------------------------------------ tiles of every size
+
+class Plan(ctypes.Structure):
+    _fields_ = [("bt", ctypes.c_int), ("split", ctypes.c_int)]
+
+
+def plan(T, n, k, kind=0):
+    """(rows of a tile, 0 where the weights are streamed; parts of the sum) of moe_fp8_linear."""
+    import mxfp4_routed_expert_amd.binding as B
+    f = B.lib._ZN3moe15fp8_linear_planEPK19moe_fp8_linear_desc
+    f.restype = Plan
+    p = f(ctypes.byref(B.Fp8LinearDesc(T, n, k, B.DT_FP8, 0, kind)))
+    return p.bt, p.split
+
+
+def forms(tiles, NT, bt, split, Kb, window, cus=256, order=None):
+    """What the tile kernel runs: a set of (16 x 16 tiles a wave has along the rows (1 to 4: up to 64, 128, 192, 256 rows), what
+    happens there): "one" or "split" sum, "window": scales of a second window of blocks within the sum, "again": not a workgroup's
+    first unit.  tiles: rows of each tile of bt.  order: the rows item by item (experts), else as one matrix goes."""
+    items = len(order) if order else len(tiles) * NT * split
+    G = min(cus, 4 * items)
+    full = items // G * G
+    tail, most = items - full, bt // 64
+    f = min(4, most) if 0 < 4 * tail <= G else min(2, most) if 0 < 2 * tail <= G else 1
+    got = set()
+
+    def unit(item, part, parts, again):
+        s = 0
+        if order:
+            rows = order[item]
+        else:
+            s, r = divmod(item, NT * len(tiles))
+            g, i = divmod(r, 4 * len(tiles))
+            rows = tiles[i // min(4, NT - 4 * g)]
+        live = min(rows - part * (bt // parts), bt // parts)
+        if live <= 0:
+            return
+        tt = (live + 63) // 64
+        a, b = Kb * s // split, Kb * (s + 1) // split
+        got.add((tt, "split" if split > 1 else "one"))
+        if any(a < w < b for w in range(window, Kb, window)):
+            got.add((tt, "window"))
+        if again:
+            got.add((tt, "again"))
+    for it in range(full):
+        unit(it, 0, 1, it >= G)
+    for u in range(f * tail):
+        unit(full + u // f, u % f, f, full > 0)
+    return got
+
+
+def linear_forms(T, n, k, kind, cus=256):
+    bt, split = plan(T, n, k)
+    if bt == 0:
+        return set()
+    return forms([min(bt, T - t) for t in range(0, T, bt)], (n + 255) // 256, bt, split, (k + 127) // 128, 32 if kind == "row" else 64, cus)
+
+
+# (T, n, k, forms that are to be among those that run; kinds of weight scales)
+EVERY = ("f32", "e8m0", "row")
+TILES = [
+    (1029, 2056, 6160, {(2, "split")}, EVERY),                                         # 128 rows, 3 parts
+    (1021, 6146, 528, {(2, "one")}, EVERY),
+    (591, 22710, 144, {(1, "again"), (2, "again"), (3, "one")}, EVERY),                # 192 rows; a second unit, cut in thirds
+    (553, 33461, 144, {(3, "again")}, EVERY),                                          # 192 rows, tile and tail
+    (7168, 2368, 272, {(3, "one"), (2, "again")}, ("f32", "row")),
+    (603, 39878, 144, {(2, "again"), (4, "again")}, EVERY),                            # 256 rows
+    (412, 16661, 992, {(3, "one"), (4, "one")}, ("f32", "e8m0")),
+    (75, 109, 4304, {(1, "split"), (1, "window")}, ("row",)),                          # windows: 32 blocks of a row's scales, 64 of a block's
+    (68, 108, 8592, {(1, "split"), (1, "window")}, ("f32", "e8m0")),
+    (66, 5338, 7872, {(2, "split"), (2, "window")}, ("row",)),
+    (1606, 259, 8944, {(2, "split"), (2, "window")}, EVERY),
+    (140, 11589, 5776, {(3, "split"), (3, "window")}, ("row",)),
+    (146, 7678, 8896, {(3, "split"), (3, "window")}, EVERY),
+    (457, 8358, 10080, {(4, "split"), (4, "window")}, EVERY),
+    (1541, 7492, 4240, {(4, "one"), (4, "window")}, ("row",)),
+    (589, 6507, 8480, {(2, "one"), (2, "window")}, ("f32",)),
+]
+
+
+def e4m3():
+    return torch.arange(256, dtype=U8).view(torch.float8_e4m3fn).double().to(DEV)
+
+
+def device_codes(n, k, seed, lead=()):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    c = torch.randint(0, 256, (*lead, n, k), generator=g, dtype=torch.uint8, device=DEV)
+    return torch.where((c & 127) == 127, torch.zeros_like(c), c)
+
+
+def values(c, s, rows):
+    """float64 values of codes [r][c] with one scale (float32 or E8M0) per rows x 128 block."""
+    s = s.double() if s.dtype is F32 else torch.exp2(s.double() - 127)
+    return e4m3()[c.long()] * s.repeat_interleave(rows, 0)[:c.shape[0]].repeat_interleave(128, 1)[:, :c.shape[1]]
+
+
+def sum_tol(x, w):
+    """test_gpu_fp8.sum_tol, on the device."""
+    top = lambda v: torch.nn.functional.pad(v.abs(), (0, -v.shape[1] % 8)).reshape(v.shape[0], -1, 8).amax(2)
+    return 7 * 2.0 ** -13 * (top(x) @ top(w).T) + (x.shape[1] / 8 + 8) * 2.0 ** -23 * (x.abs() @ w.abs().T)
+
+
+def check(y, ref, tol, res, what):
+    """test_gpu_fp8.check_product's tolerance, every value of y."""
+    if res is not None:
+        ref = ref + res.double()
+        tol = tol + 2.0 ** -24 * (ref.abs() + res.double().abs())
+    if y.dtype is BF:
+        tol = tol * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()
+    over = (y.double() - ref).abs() > tol + 1e-30
+    assert not over.any(), f"{what}: {int(over.sum())} values, first {over.nonzero()[0].tolist()}"
+
+
+@pytest.mark.parametrize("T,n,k,want,kind", [(*c[:4], kind) for c in TILES for kind in c[4]],
+                         ids=[f"{c[0]}x{c[1]}x{c[2]}-{kind}" for c in TILES for kind in c[4]])
+def test_tiles(M, T, n, k, want, kind):
+    cus = torch.cuda.get_device_properties(0).multi_processor_count
+    assert want <= linear_forms(T, n, k, kind, cus)
+    x = hidden(T, k, T + n)
+    c, s, _, _ = M.moe_fp8_quantize(x.to(DEV))
+    w = device_codes(n, k, n + k)
+    ws = scales_of(kind, n, k, n).to(DEV)
+    xv, wv = values(c, s, 1), values(w, ws, 1 if kind == "row" else 128)
+    ref, tol = xv @ wv.T, sum_tol(xv, wv)
+    del wv
+    res = torch.randn(T, n, generator=torch.Generator(device=DEV).manual_seed(T), device=DEV) * float(ref.abs().mean())
+    for dt in (BF, F32):
+        y = M.moe_fp8_linear(c, w, ws, x_scales=s, out_dtype=dt)
+        check(y, ref, tol, None, f"{kind} {dt}")
+        # results in a buffer with a guard around them, added to what is there
+        buf = torch.full((64 + T * n + 64,), 7.0, dtype=dt, device=DEV)
+        acc = buf[64:64 + T * n].view(T, n)
+        acc.copy_(res)
+        r = acc.clone()
+        M.moe_fp8_linear(c, w, ws, x_scales=s, residual=acc, out=acc)
+        assert (buf[:64] == 7).all() and (buf[64 + T * n:] == 7).all()
+        check(acc, ref, tol, r, f"{kind} {dt} with residual")
+        assert torch.equal(M.moe_fp8_linear(c, w, ws, x_scales=s, out_dtype=dt), y), "the same bits again"
+
+
+@pytest.mark.parametrize("T,n,k", [(1021, 2048, 6144), (2045, 7168, 2368)])
+def test_layer_gradients_in_tiles(M, T, n, k):
+    """A training step's three products, each in tiles above 64 rows, five column tiles and more."""
+    for a in ((T, n, k), (T, k, n), (n, k, (T + 15) // 16 * 16)):
+        assert plan(*a)[0] > 64
+    w, x, dy = (hidden(n, k, 1) * 0.1).to(DEV), hidden(T, k, 2).to(DEV), hidden(T, n, 3).to(DEV)
+    layer = M.FP8Linear(w, T, dw_dtype=F32)
+    y = layer.forward(x)
+    wc, wsc, wct, wst = layer.w_q
+    xq, dyq = M.moe_fp8_quantize(x, cols=True), M.moe_fp8_quantize(dy, cols=True)
+    wv = values(wc, wsc, 128)
+    a = values(*xq[:2], 1)
+    check(y, a @ wv.T, sum_tol(a, wv), None, "y")
+    dx, dw = layer.backward(dy)
+    g, wt = values(*dyq[:2], 1), values(wct, wst, 128)
+    assert torch.equal(wt, wv.T)
+    check(dx, g @ wv, sum_tol(g, wt), None, "dx")
+    gt, xt = values(*dyq[2:], 1), values(*xq[2:], 1)
+    check(dw, gt @ xt.T, sum_tol(gt, xt), None, "dw")
+
+
+@pytest.mark.parametrize("T,n,k,tt", [(4500, 2048, 1040, 1), (8300, 1024, 1040, 2), (4500, 2304, 5120, 3), (4500, 4096, 4096, 4)])
+def test_weight_gradient_of_many_tokens(M, T, n, k, tt):
+    """More than 4096 tokens: a second window of scales along the sum, whole and in parts, in tiles of 64 to 256 rows."""
+    assert (tt, "window") in linear_forms(n, k, (T + 15) // 16 * 16, "row", torch.cuda.get_device_properties(0).multi_processor_count)
+    x, dy = hidden(T, k, 5).to(DEV), hidden(T, n, 6).to(DEV)
+    layer = M.FP8Linear((hidden(n, k, 7) * 0.1).to(DEV), T)
+    layer.forward(x)
+    dw = layer.backward(dy)[1]
+    gt, xt = values(*M.moe_fp8_quantize(dy, rows=False, cols=True)[2:], 1), values(*M.moe_fp8_quantize(x, rows=False, cols=True)[2:], 1)
+    check(dw, gt @ xt.T, sum_tol(gt, xt), None, "dw")
+
+
+# ------------------------------------------------------------------ experts in tiles of every size
+
+def device_experts(M, E, H, I, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    m, s = {}, {}
+    for i, (name, n, k) in enumerate((("gate", I, H), ("up", I, H), ("down", H, I))):
+        m[name] = device_codes(n, k, seed + 7 * i, (E,))
+        s[name] = (torch.rand(E, n // 128, k // 128, generator=g, device=DEV) + 0.5) * (0.01 * k ** -0.5)
+    w = M.ExpertWeights("fp8b128", H, I, m["gate"], s["gate"], m["up"], s["up"], m["down"], s["down"])
+    return w, lambda name, e: values(m[name][e], s[name][e], 128)
+
+
+def check_expert_rows(M, w, value, x, k, offs, sp, o):
+    """h, its codes and y of every row against 64 bits; o: the offsets on the host (one expert: [0, T])."""
+    T = x.shape[0]
+    h, hq, hs = M.moe_expert_gateup(w, x, "fp8", k, offs, sp)
+    y = M.moe_expert_down(w, T, "fp8", k, offs, None, hq, hs)
+    xv = values(*M.moe_fp8_quantize(x)[:2], 1)
+    hv = values(hq, hs, 1)
+    for e in range(len(o) - 1):
+        if o[e] == o[e + 1]:
+            continue
+        r = slice(o[e], o[e + 1])
+        a = xv if sp is None else xv[sp[r].long() // k]
+        wg, wu = value("gate", e), value("up", e)
+        g, u, eg, eu = a @ wg.T, a @ wu.T, sum_tol(a, wg), sum_tol(a, wu)
+        ref = g / (1 + torch.exp(-g)) * u
+        # |silu'| <= 1.1, |silu(g)| <= |g|; exp2, reciprocal and three products: 8 roundings
+        tol = 1.1 * eg * u.abs() + g.abs() * eu + eg * eu + 2.0 ** -20 * ref.abs()
+        assert ((h[r].double() - ref).abs() <= tol + 1e-30).all(), f"h of expert {e}"
+        wd = value("down", e)
+        check(y[r], hv[r] @ wd.T, sum_tol(hv[r], wd), None, f"y of expert {e}")
+    live = slice(0, o[-1])
+    c, s, _, _ = M.moe_fp8_quantize(h)
+    assert torch.equal(c[live], hq[live]) and torch.equal(s[live], hs[live])
+    assert torch.equal(M.moe_expert_ffn(w, x, "fp8", k, offs, sp)[live], y[live])
+
+
+def expert_forms(counts, N, pair, Kb):
+    cols = 128 if pair else 256
+    order = [min(256, c - t) for c in counts for _ in range((N + cols - 1) // cols) for t in range(0, c, 256)]
+    return forms(None, None, 256, 1, Kb, 64, torch.cuda.get_device_properties(0).multi_processor_count, order)
+
+
+# rows of an expert, in turn
+COUNTS = [256, 250, 193, 192, 130, 128, 65, 64, 1, 0, 300, 449, 17, 201, 100, 129]
+
+
+@pytest.mark.parametrize("E,H,I,want_pair,want_down", [
+    (32, 1280, 640, {(1, "one"), (2, "one"), (3, "one"), (4, "one")}, {(1, "one"), (2, "one"), (3, "one"), (4, "one")}),
+    (64, 1280, 768, {(4, "one"), (3, "one"), (1, "again")}, {(4, "one"), (1, "again")}),
+    (16, 8320, 1280, {(4, "window"), (3, "window"), (2, "window"), (1, "window")}, {(4, "again"), (2, "again")}),
+    (16, 2560, 8320, {(4, "again"), (3, "again"), (2, "again")}, {(4, "window"), (3, "window"), (2, "window"), (1, "window")})])
+def test_experts_in_tiles(M, E, H, I, want_pair, want_down):
+    k = 2
+    counts = [COUNTS[(e + e // 16) % 16] for e in range(E)]
+    if sum(counts) % k:
+        counts[0] -= 1
+    # the pairs' experts in an order in which no token has one twice
+    flat = torch.tensor([e for e in range(E) for _ in range(counts[e])], dtype=torch.int32)
+    T = len(flat) // k
+    ids = torch.stack([flat[:T], flat[T:]], 1)
+    assert (ids[:, 0] != ids[:, 1]).all()
+    assert want_pair <= expert_forms(counts, I, True, H // 128), expert_forms(counts, I, True, H // 128)
+    assert want_down <= expert_forms(counts, H, False, I // 128), expert_forms(counts, H, False, I // 128)
+    w, value = device_experts(M, E, H, I, 3)
+    offs, sp, _ = M.moe_permute(ids[torch.randperm(T, generator=torch.Generator().manual_seed(1))].contiguous().to(DEV), E)
+    o = offs.tolist()
+    assert [b - a for a, b in zip(o, o[1:])] == counts
+    check_expert_rows(M, w, value, hidden(T, H, 9).to(DEV), k, offs, sp, o)
+
+
+@pytest.mark.parametrize("T,H,I,want", [(1930, 256, 2560, {(3, "one"), (4, "one")}), (100, 256, 16640, {(2, "one")}), (200, 128, 33280, {(4, "one"), (1, "again")})])
+def test_shared_expert_in_tiles(M, T, H, I, want):
+    """gate and up of one matrix (the identity form) above 64 rows."""
+    bt = 256 if T > 128 else 128
+    assert want <= forms([min(bt, T - t) for t in range(0, T, bt)], I // 128, bt, 1, H // 128, 64, torch.cuda.get_device_properties(0).multi_processor_count)
+    w, value = device_experts(M, 1, H, I, 5)
+    check_expert_rows(M, w, value, hidden(T, H, 10).to(DEV), 1, None, None, [0, T])
