@@ -1081,7 +1081,7 @@ def moe_block_norm(z, w_after=None, gate=None, residual=None, w_before=None, res
     sshape = (T, (d + 127) // 128)
     if not (z.is_cuda and z.dtype in DT and z.is_contiguous() and _fits(dev, w_after, f32, (d,)) and _fits(dev, w_before, f32, (d,))
             and _fits(dev, residual, yt, (T, d)) and (gate is None or _fits(dev, gate, f32, gate.shape))
-            and (rng is None or (rng.dtype in _RNG and _fits(dev, rng, rng.dtype, (2,))))
+            and _fits(dev, rng, _one_of(rng, _RNG), (2,))
             and (out is None or (_fits(dev, oy, yt, (T, d)) and _fits(dev, ou, bf, (T, d)) and _fits(dev, oc, u8, (T, d)) and _fits(dev, os_, u8, sshape)))):
         _operands(dev, (z, _one_of(z, DT), "z", None), (w_after, f32, "w_after", (d,)), (w_before, f32, "w_before", (d,)),
                   (gate, f32, "gate", None), (residual, yt, "residual", (T, d)), (rng, _one_of(rng, _RNG), "rng", (2,)),
@@ -1126,7 +1126,7 @@ def moe_block_norm_backward(z, w_after=None, gate=None, y=None, w_before=None, d
     bf = torch.bfloat16
     if not (ref.is_cuda and _fits(dev, z, zt, (T, d)) and _fits(dev, w_after, f32, (d,)) and _fits(dev, w_before, f32, (d,))
             and (gate is None or _fits(dev, gate, f32, gate.shape)) and _fits(dev, y, yt, (T, d)) and _fits(dev, du, bf, (T, d))
-            and _fits(dev, dy, yt, (T, d)) and (rng is None or (rng.dtype in _RNG and _fits(dev, rng, rng.dtype, (2,))))
+            and _fits(dev, dy, yt, (T, d)) and _fits(dev, rng, _one_of(rng, _RNG), (2,))
             and (out is None or all(_fits(dev, t, dt, sh) for t, dt, sh in zip(o, types, shapes)))):
         _operands(dev, (ref, _one_of(ref, DT), "z", (T, d)), (z, zt, "z", (T, d)), (w_after, f32, "w_after", (d,)),
                   (w_before, f32, "w_before", (d,)), (gate, f32, "gate", None), (y, yt, "y", (T, d)), (du, bf, "du", (T, d)),

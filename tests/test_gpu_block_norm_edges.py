@@ -185,3 +185,16 @@ def test_backward_first_rows_that_are_walked(M, T, d):
     """A row more than a backward launch has waves (1024) or workgroups (256)."""
     check_backward(M, T, d, BF, F32, True, True, "token", 0.1, True)
     check_backward(M, T, d, F32, BF, True, False, "channel", 0.0, True)
+
+
+def test_random_numbers_that_are_no_tensor_are_refused(M):
+    z = torch.zeros(4, 64, device=DEV)
+    for rng, err in (([1, 2], TypeError), (torch.tensor([1, 2], dtype=torch.int32, device=DEV), TypeError), (torch.tensor([1, 2]), ValueError),
+                     (torch.tensor([1, 2, 3], device=DEV), ValueError)):
+        with pytest.raises(err, match="rng"):
+            M.moe_block_norm(z, dropout=0.5, rng=rng)
+        with pytest.raises(err, match="rng"):
+            M.moe_block_norm_backward(z, dy=z, dropout=0.5, rng=rng, y_dtype=F32)
+    one = torch.tensor([1, 2], device=DEV)
+    a, b = (M.moe_block_norm(z + 1, dropout=0.5, rng=r)[0] for r in (one, one.view(torch.uint64)))
+    assert torch.equal(a, b)
