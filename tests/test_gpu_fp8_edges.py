@@ -284,3 +284,36 @@ def test_shared_expert_in_tiles(M, T, H, I, want):
     assert want <= forms([min(bt, T - t) for t in range(0, T, bt)], I // 128, bt, 1, H // 128, 64, torch.cuda.get_device_properties(0).multi_processor_count)
     w, value = device_experts(M, 1, H, I, 5)
     check_expert_rows(M, w, value, hidden(T, H, 10).to(DEV), 1, None, None, [0, T])
+
+
+# ------------------------------------------------------------------ a layer's step in a graph
+
+@pytest.mark.parametrize("T", [1, 4, 70, 300])
+def test_captured_layer_with_fp8_activations(M, T):
+    """MoELayer(act="fp8") and the norms around it in one graph, with eager steps of the same layer in between."""
+    E, k, H, I = 8, 2, 256, 128
+    w, _ = device_experts(M, E, H, I, 5)
+    sh, _ = device_experts(M, 1, H, 256, 6)
+    g = torch.Generator().manual_seed(9)
+    wr, wsg = (torch.randn(E, H, generator=g) * 0.1).to(BF).to(DEV), (torch.randn(H, generator=g) * 0.1).to(BF).to(DEV)
+    wb, wa = torch.rand(H, generator=g).to(DEV) + 0.5, torch.rand(H, generator=g).to(DEV) + 0.5
+    layer = M.MoELayer(M.LayerWeights("sigmoid", k, True, 1.0, "fp8", wr, w, shared=sh, w_shared_gate=wsg), T, DEV)
+    res = hidden(T, H, 10).to(DEV)
+
+    def step():
+        u = M.moe_block_norm(res, w_before=wb, want_y=False)[1]
+        return M.moe_block_norm(layer.forward(u), w_after=wa, residual=res, w_before=wb, want_codes=True)
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for i in range(4):
+        res.copy_(hidden(T, H, 20 + i))
+        graph.replay()
+        got = [t.clone() for t in (*out, layer.ids, layer.out)]
+        torch.cuda.synchronize()
+        for a, b in zip(got, (*step(), layer.ids, layer.out)):
+            assert torch.equal(a, b)
