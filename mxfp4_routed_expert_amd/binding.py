@@ -169,7 +169,9 @@ def _stream():
 
 
 def _need(t, dtype, name, shape=None):
-    if t is None:
+    # (one expression a tensor when all is well: a decoded token's step is a few dozen microseconds of the host)
+    if t is None or (type(t) is torch.Tensor and t.is_cuda and (dtype is None or t.dtype is dtype) and t.is_contiguous()
+                     and (shape is None or t.shape == shape)):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -185,7 +187,9 @@ def _need(t, dtype, name, shape=None):
 
 def _room(t, dtype, name, n):
     """An optional tensor that a call reads or writes n elements of: of dtype, contiguous, no shorter, in device memory."""
-    if t is not None and isinstance(t, torch.Tensor) and t.dtype == dtype and t.numel() < n:
+    if t is None or (type(t) is torch.Tensor and t.dtype is dtype and t.numel() >= n and t.is_cuda and t.is_contiguous()):
+        return
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.numel() < n:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, room for {n} values is needed")
     _need(t, dtype, name)
 
@@ -1034,13 +1038,15 @@ def _gate_kind(gate, T, d):
 
 
 def _constant(v):
-    """A number (or what holds one, such as a tensor of one element) as the C side's float, its value at this call; -0 as 0."""
-    return _f32(v).value + 0.0
+    """A number, or what holds one (such as a tensor of one element), as the C side's float: its value at this call."""
+    return _f32(v).value
 
 
 def _norm_desc(T, d, zt, yt, kind, eps, residual_scale, dropout):
-    # (values, not objects: a tensor is the same key after its value has changed)
-    return _norm_plan(T, d, zt, yt, kind, _constant(eps), _constant(residual_scale), _constant(dropout))
+    # (values, not objects: a tensor is the same key after its value has changed; -0 as 0, which is the same key)
+    if not type(eps) is type(residual_scale) is type(dropout) is float:
+        eps, residual_scale, dropout = _constant(eps), _constant(residual_scale), _constant(dropout)
+    return _norm_plan(T, d, zt, yt, kind, eps, residual_scale + 0.0, dropout)
 
 
 @functools.lru_cache(maxsize=4096)
