@@ -362,9 +362,10 @@ def moe_expert_ffn(w: ExpertWeights, x, act="float", k=1, expert_offsets=None, s
     T = x.shape[0]
     _need(x, None, "x", (T, w.d_model))
     _need(expert_offsets, torch.int32, "expert_offsets", (w.num_experts + 1,))
-    _need(sorted_pairs, torch.int32, "sorted_pairs")
     c = w.c_struct()
     R = T * k if expert_offsets is not None else T
+    _room(sorted_pairs, torch.int32, "sorted_pairs", R)
+    _need(ws, None, "ws")
     y = out if out is not None else torch.empty((R, w.d_model), dtype=torch.float32, device=x.device)
     _need(y, torch.float32, "y_rows", (R, w.d_model))
     kk = k if expert_offsets is not None else 1

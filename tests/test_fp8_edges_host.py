@@ -43,19 +43,18 @@ def _experts(fmt, E=2, H=256, I=128):
     return B.ExpertWeights(fmt, H, I, u8(E, I, H // 2), u8(E, I, H // 32), u8(E, I, H // 2), u8(E, I, H // 32), u8(E, H, I // 2), u8(E, H, I // 32))
 
 
-@pytest.mark.parametrize("act,fmt,codes,scales", [("fp8", "fp8b128", 128, 1), ("mxfp4", "mxfp4", 64, 4), ("float", "mxfp4", 64, 4)])
-def test_experts_refuse_short_buffers(monkeypatch, act, fmt, codes, scales):
-    """Buffers of another mode, or a row short, are refused before a kernel could run past their end."""
-    class Reached(Exception):
-        pass
+class Reached(Exception):
+    """A call got past its checks to the library."""
 
+
+@pytest.fixture
+def host(monkeypatch):
+    """The binding with host tensors: all but the place of a tensor is checked, and the library is not called."""
     class Lib:
         def __getattr__(self, name):
             if name.endswith("_workspace"):
                 return lambda *a: 16
             raise Reached(name)
-    monkeypatch.setattr(B, "lib", Lib())
-    # (host tensors: all but the place of a tensor is checked here)
     need = B._need
 
     def anywhere(t, dtype, name, shape=None):
@@ -66,7 +65,13 @@ def test_experts_refuse_short_buffers(monkeypatch, act, fmt, codes, scales):
                 raise
             if dtype is not None and t.dtype != dtype:
                 raise TypeError(f"{name} must be {dtype}")
+    monkeypatch.setattr(B, "lib", Lib())
     monkeypatch.setattr(B, "_need", anywhere)
+
+
+@pytest.mark.parametrize("act,fmt,codes,scales", [("fp8", "fp8b128", 128, 1), ("mxfp4", "mxfp4", 64, 4), ("float", "mxfp4", 64, 4)])
+def test_experts_refuse_short_buffers(host, act, fmt, codes, scales):
+    """Buffers of another mode, or a row short, are refused before a kernel could run past their end."""
     w, T, k = _experts(fmt), 3, 2
     R, H, I = T * k, w.d_model, w.d_ff
     x = torch.zeros(T, H, dtype=torch.bfloat16)
@@ -103,6 +108,11 @@ def test_experts_refuse_short_buffers(monkeypatch, act, fmt, codes, scales):
         down(y=y[:R - 1])
     with pytest.raises(TypeError, match="y_rows"):
         down(y=y.bfloat16())
+    ffn = lambda sp=sp, ws=None: B.moe_expert_ffn(w, x, act, k, offs, sp, ws=ws)
+    with pytest.raises(ValueError, match="sorted_pairs"):
+        ffn(sp=sp[:R - 1])
+    with pytest.raises(Reached):
+        ffn()
     # buffers of more rows are taken, as before
     with pytest.raises(Reached):
         gateup(h=torch.zeros(R + 1, I), hq=u8(R + 1, codes), hs=u8(R + 1, scales))
