@@ -206,7 +206,16 @@ typedef struct {
  * act == MOE_ACT_MXFP4: x and h are MX-quantised (OCP MX v1.0: scale 2^(floor(log2 amax)-2),
  *   round to nearest even, saturate at 6) and the products use the block-scaled FP4
  *   matrix instructions; MXFP4 weights only (else MOE_ERR_UNSUPPORTED).
- * ws: moe_expert_ffn_workspace(w, act, T, k) bytes (k ignored in the identity form).
+ * act == MOE_ACT_FP8: x and h are quantised to E4M3 per 128 values (moe_fp8_quantize), the products run on
+ *   the FP8 matrix cores with the weights' float32 block scales; MOE_W_FP8_E4M3_B128 only (else
+ *   MOE_ERR_UNSUPPORTED); x, y_rows, weight codes and workspace 16-byte aligned.  Their sums of 8 products lose
+ *   what moe_fp8_linear states (about 2e-5 of a result), float32 y_rows included.  Gate and up of few rows (up to
+ *   8 an expert where experts are many, up to 64 rows of a tile) are multiplied exactly instead: h falls on the
+ *   8-bit code of its float32 value there, and now and then on the next one (6 to 12 % off) in larger tiles.  So a
+ *   token's result depends within that on how many rows its expert has, and on the number of compute units; the
+ *   same call gives the same bits.
+ * ws: moe_expert_ffn_workspace(w, act, T, k) bytes (k ignored in the identity form); with MOE_ACT_FP8 a workspace
+ *   for T and k serves fewer of either.
  */
 moe_status moe_expert_ffn(const moe_expert_weights *w, int32_t act, int32_t T, int32_t k,
                           const void *x, int32_t x_dtype, const int32_t *expert_offsets,
@@ -223,8 +232,7 @@ size_t moe_expert_ffn_workspace(const moe_expert_weights *w, int32_t act, int32_
  *   MOE_ACT_FP8:   h_codes uint8 [R][d_ff] (16-byte aligned) and h_scales uint8 [R][d_ff/128] required (h quantised
  *                  as by moe_fp8_quantize); h (float32, before quantisation, 16-byte aligned) optional.
  *                  R / 256 + num_experts at most 65535.
- *   ws: moe_expert_gateup_workspace(w, act, T, k) bytes (k ignored in the identity form); as moe_expert_ffn's, a workspace for T
- *       and k serves fewer of either.
+ *   ws: moe_expert_gateup_workspace(w, act, T, k) bytes (k ignored in the identity form; fewer tokens: as moe_expert_ffn).
  * moe_expert_down writes y_rows[r] = down_e . h[r] from h (FLOAT) or h_codes/h_scales (MXFP4, FP8).
  */
 moe_status moe_expert_gateup(const moe_expert_weights *w, int32_t act, int32_t T, int32_t k,
@@ -498,15 +506,15 @@ moe_status moe_mxfp8_dequant(int32_t rows, int32_t cols, const uint8_t *codes, c
  * smallest integer for which the block's largest finite magnitude is at most 448 * 2^X, kept in [-127, 127]
  * (byte 0 for an all-zero block); codes = nearest E4M3 of v / 2^X, ties to even; NaN and infinities become NaN codes
  * and take no part in the scale.  A row's or column's last block may be shorter.  Every matrix has fewer than 2^31
- * elements; values, codes, results and workspaces are 16-byte aligned.  Results depend on the arguments alone (sums have a
- * fixed order; no atomics); the workspace rules of the dense layers above hold.
+ * elements; values, codes, results and workspaces are 16-byte aligned.  Results depend on the arguments and the number of
+ * compute units alone (sums have a fixed order; no atomics); the workspace rules of the dense layers above hold.
  *
  * moe_fp8_quantize -- rows [rows][cols] (bf16 or float32, cols a multiple of 8; of 16 for moe_fp8_linear) to either or both of
  *   codes uint8 [rows][cols], scales uint8 [rows][ceil(cols/128)]: blocks along the row (forward and input-gradient
  *     products);
  *   codes_t uint8 [cols][ld], scales_t uint8 [cols][ceil(rows/128)], ld = rows rounded up to a multiple of 16, zeros past
  *     `rows`: the transposed matrix with blocks along the column (weight-gradient products, which sum over the rows).
- *   With both, the values are read once.
+ *   With both, the values are read once.  Transposed codes, and weights, of at most 65535 * 128 rows.
  * moe_fp8_quantize_weight -- a weight [n][kdim] (bf16 or float32, kdim a multiple of 16) to 128 x 128 blocks, by the same
  *   rule with the whole block's largest magnitude: codes [n][kdim] with scales [ceil(n/128)][ceil(kdim/128)], and / or the
  *   same codes transposed, codes_t [kdim][ld] (ld = n rounded up to 16, zeros past n) with scales_t
@@ -554,7 +562,7 @@ size_t moe_fp8_linear_workspace(const moe_fp8_linear_desc *desc);
  *   n = w_after ? z r(z) w_after : z
  *   y = residual_scale * residual + gate * m * n               (no residual: gate * m * n), rounded to y_dtype
  *   u = y r(y) w_before                                        of the rounded y, rounded to bf16
- *   u_codes, u_scales: u as moe_fp8_quantize writes it.
+ *   u_codes, u_scales: u as moe_fp8_quantize writes it, an x of moe_fp8_linear (the experts' calls take u and quantise it).
  *   m = 0 or 1 / (1 - p): dropout.  Element e = t d + c draws 16 bits: Philox4x32-10 with key rng[0] (low word, high word)
  *   and counter (e / 8 low, e / 8 high, rng[1] low, rng[1] high); elements 8 i .. 8 i + 7 take the low and high halves
  *   of its four words in order; an element stays when its bits >= 65536 p, and else its m n is 0, also where n is NaN or

@@ -16,8 +16,8 @@
 // partial row a workgroup and are added in order by a second kernel: no atomics, the same bits every time.
 //
 // Bound by HBM.  8192 x 7168 bf16 with both norms, a channel gate, dropout and a residual: forward 94 us (5.0 TB/s; a copy
-// 5.0 to 5.7 by card), backward with all gradients 138 us (5.1 TB/s).  Two rows in flight instead of one: the same.  512
-// workgroups forward; 256 backward, since each adds a partial row of 8 d bytes: 509 x 6144 takes 15 us and 3 for the sums.
+// 5.0 to 5.7 by card), backward with all gradients 136 us (5.2 TB/s).  Two rows in flight instead of one: the same.  512
+// workgroups forward; 256 backward, since each adds a partial row of 8 d bytes: 509 x 6144 takes 15 us and 4 for the sums.
 #include <algorithm>
 #include <initializer_list>
 

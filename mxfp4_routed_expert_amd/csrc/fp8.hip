@@ -1,5 +1,5 @@
 // moe_fp8_linear: the product of block-128 FP8 operands, its argument checks and its plan.
-// Few rows stream the weights (fp8_stream.hip; up to 16 short rows in one launch: 2048 x 7168 for one row 7.9 us); above, rows to
+// Few rows stream the weights (fp8_stream.hip; up to 16 short rows in one launch: 2048 x 7168 for one row 7.5 to 8.0 us); above, rows to
 // codes, tiles, and the sum of parts where there are few tiles.
 #include <algorithm>
 
@@ -12,8 +12,13 @@ namespace {
 // compute units.  A step is one block of a tile: 1.55 us for 256 rows with every unit at work (measured from long sums, 1.3 with
 // E8M0 scales), 0.6 of that with few.  A tile's start and end are 4 us and, when all write at once, 15 for 256 rows.  The tiles
 // of a last, short round are halved or quartered.  Parts are written, and read by a second launch, at 6.5 TB/s.  Measured
-// (us; [rows, parts]): 333 x 2368 x 7168 [128,4] 25.6, [128,8] 24.3, [256,3] 28.6, [64,3] 30.6; 1021 x 6144 x 2048 [128,1] 22.8,
-// [256,1] 23.8, [192,1] 28.9, [128,2] 37.1; 4096 x 7168 x 7168 [256,1] 204, [192,1] 232, [128,1] 290.
+// (us, x as codes; [rows, parts], what is taken first): 333 x 2368 x 7168 [64,4] 25.0, [128,4] 24.9, [128,8] 23.7, [256,6] 25.0,
+// [64,3] 29.2; 1021 x 6144 x 2048 [128,1] 21.9, [256,1] 22.0, [192,1] 27.2, [64,1] 29.2, [128,2] 37.1; 1021 x 2048 x 6144 [128,3] 29.2,
+// [256,2] 27.0, [128,2] 27.2, [256,1] 33.8; 2048 x 2368 x 7168 [128,1] 51.7, [192,2] 48.7, [256,1] 52.1, [64,1] 72.8; 2048 x 7168 x
+// 2368 [256,1] 41.1, [128,1] 48.8, [192,1] 50.7; 7168 x 2368 x 2048 [192,1] 51.8, [256,1] 53.8, [128,1] 62.7; 4096 x 7168 x 7168 [256,1]
+// 208, [192,1] 235, [128,1] 286; 200 x 2048 x 7168 [64,4] 24.7, [128,6] 21.3; 128 x 7168 x 2048 [64,1] 22.9, [128,3] 18.6.  So the choice is
+// within 8 % of the best of these, but for few tiles, whose steps and starts take longer than the estimate says (tiles of 64 rows
+// do not take turns): there more parts would take 14 to 19 % less.
 using Plan = Fp8Plan;
 Plan plan_of(int R, int N, int Kb) {
     constexpr int G = 256;
@@ -43,9 +48,10 @@ struct Layout {
     Plan plan = {256, 1};
 };
 // Few rows stream the weights.  Every workgroup of 16 columns or more reads all of x, so it depends on the product's size from 17
-// rows on.  Both sides, us (tiles second): 2048 x 7168, 17 rows 14.4, 18.7, 64 rows 25.8, 24.3; 7168 x 2048, 64 rows 21.4, 30.6;
-// 6144 x 4096, 32 rows 22.8, 24.3, 48 rows 30.9, 25.5; 7168 x 7168, 17 rows 23.8, 27.1, 32 rows 29.6, 28.1; 512 x 512, 64 rows
-// 7.0, 11.9; 131072 x 1024, 17 rows 53.6, 47.1.
+// rows on.  Both sides, us (streamed; tiles as plan_of gives them; tiles of the best number of parts, where it gives another): 2048 x 7168,
+// 17 rows 14.2, 18.7, 64 rows 25.8, 22.6; 7168 x 2048, 64 rows 20.9, 24.8, 19.4; 6144 x 4096, 32 rows 22.4, 22.0, 18.5, 48 rows
+// 30.9, 23.2, 20.0; 7168 x 7168, 17 rows 23.2, 27.1, 22.4; 512 x 512, 64 rows 7.0, 11.9; 131072 x 1024, 17 rows 50.5, 43.3.  The border
+// lies where the first two meet, 64 short wide rows apart.
 bool few_rows(const moe_fp8_linear_desc *d) {
     return d->T <= kFp8RowsMax || (d->T <= 64 && (int64_t)d->T * d->n * d->kdim <= (int64_t)1 << 30);
 }

@@ -3,9 +3,10 @@
 // other axis; and the values back.
 //
 // All of it is bound by HBM: one read, and one byte a value for each form written.  4096 x 7168 bf16 to rows of codes 19 us
-// (4.6 TB/s); 2048 x 7168 both ways 18 us (3.1 TB/s: one tile a workgroup, all of them resident, so that the reads come first
+// (4.5 TB/s); 2048 x 7168 both ways 17 to 19 us (3.1 to 3.5 TB/s: one tile a workgroup, all of them resident, so that the reads come first
 // and the writes after, and what is written is of a size that a plain fill takes at 4.8 TB/s); a weight of 7168 x 2368 with its
-// transpose 16 us (4.2 TB/s).
+// transpose 16 to 18 us (4.0 TB/s).  2048 x 2368 both ways takes 9 to 10 us (2.2 TB/s: 304 tiles, little over one a CU).
+// 4096 x 7168 codes back to bf16 18 us, to float32 31 (4.8 TB/s).
 #include "fp8.h"
 
 namespace moe {
