@@ -1,6 +1,7 @@
 """Norms around a block at their edges (GPU): constants that change, magnitudes, masked places, rows walked one behind the other."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
@@ -198,3 +199,43 @@ def test_random_numbers_that_are_no_tensor_are_refused(M):
     one = torch.tensor([1, 2], device=DEV)
     a, b = (M.moe_block_norm(z + 1, dropout=0.5, rng=r)[0] for r in (one, one.view(torch.uint64)))
     assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ the largest sizes
+
+def test_largest_rows(M):
+    """Just under 2^31 values: the last rows as those rows by themselves, and the counter's bits there."""
+    T, d, at, p = 262143, 8184, 262140, 0.25
+    seed, off = 5, 6
+    g = torch.Generator(device=DEV).manual_seed(1)
+    r = lambda *s: torch.randn(*s, dtype=BF, device=DEV, generator=g)
+    z, res, wa, wb, ch = r(T, d), r(T, d), rnd(2, d).abs().to(DEV) + 0.3, rnd(3, d).abs().to(DEV) + 0.3, rnd(4, 1, d).to(DEV)
+    end = lambda t: t[at:].clone()
+    kw = dict(w_after=wa, gate=ch, w_before=wb)
+    got = M.moe_block_norm(z, residual=res, want_codes=True, **kw)
+    few = M.moe_block_norm(end(z), residual=end(res), want_codes=True, **kw)
+    for a, b in zip(got, few):
+        assert torch.equal(a[at:], b)
+    y = got[0]
+    del got
+    # dropout: which elements stay in the last rows, from the counter
+    b = np.arange(at * d // 8, T * d // 8, dtype=np.uint64)
+    ctr = np.stack([b & np.uint64(0xFFFFFFFF), b >> np.uint64(32), np.full_like(b, off), np.zeros_like(b)], -1)
+    words = R.philox4x32_10(ctr, (seed, 0))
+    kept = np.stack([words & np.uint64(0xFFFF), words >> np.uint64(16)], -1).reshape(T - at, d) >= int(p * 65536)
+    rng = torch.tensor([seed, off], device=DEV)
+    one = M.moe_block_norm(z.fill_(1.0), dropout=p, rng=rng)[0]
+    assert torch.equal(one[at:].cpu() != 0, torch.from_numpy(kept))
+    del one
+    z.copy_(res)
+    du, dy = r(T, d), r(T, d)
+    got = M.moe_block_norm_backward(z, y=y, du=du, dy=dy, want=("dz", "dresidual", "dw_before"), **kw)
+    few = M.moe_block_norm_backward(end(z), y=end(y), du=end(du), dy=end(dy), want=("dz", "dresidual", "dw_before"), **kw)
+    assert torch.equal(got[0][at:], few[0]) and torch.equal(got[1][at:], few[1])
+    # dw_before: a sum over all rows, each partial row (1024 and fewer terms) and their sum within T + 16 roundings of the magnitudes
+    want, mag = torch.zeros(d, dtype=torch.float64, device=DEV), torch.zeros(d, dtype=torch.float64, device=DEV)
+    for t in range(0, T, 8192):
+        yb, db = y[t:t + 8192].double(), du[t:t + 8192].double()
+        term = db * yb * torch.rsqrt((yb * yb).mean(1, keepdim=True) + 1e-6)
+        want, mag = want + term.sum(0), mag + term.abs().sum(0)
+    assert ((got[4].double() - want).abs() <= (4 * REL + (T + 16) * 2.0 ** -24) * mag).all()

@@ -317,3 +317,80 @@ def test_captured_layer_with_fp8_activations(M, T):
         torch.cuda.synchronize()
         for a, b in zip(got, (*step(), layer.ids, layer.out)):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ the largest sizes
+
+def test_largest_rows(M):
+    """Just under 2^31 values: both quantised forms, their values, and a product, at the last rows as those rows by themselves."""
+    T, d, at = 131071, 16368, 130944                           # (the last block of 128 rows is a row short)
+    x = torch.randn(T, d, dtype=BF, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    end = x[at:].clone()
+    c, s, ct, st = M.moe_fp8_quantize(x, cols=True)
+    rc, rs, rct, rst = M.moe_fp8_quantize(end, cols=True)
+    assert torch.equal(c[at:], rc) and torch.equal(s[at:], rs) and torch.equal(ct[:, at:], rct) and torch.equal(st[:, -1:], rst)
+    del ct, st
+    c2, s2, _, _ = M.moe_fp8_quantize(x)
+    assert torch.equal(c2, c) and torch.equal(s2, s)
+    del c2, s2
+    v = M.moe_fp8_dequant(c, s)
+    assert torch.equal(v[at:], M.moe_fp8_dequant(rc, rs))
+    del v
+    n = 272
+    w, ws = device_codes(n, d, 2), scales_of("f32", n, d, 3).to(DEV)
+    xv, wv = values(rc, rs, 1), values(w, ws, 128)
+    ref, tol = xv @ wv.T, sum_tol(xv, wv)
+    check(M.moe_fp8_linear(c, w, ws, x_scales=s)[at:], ref, tol, None, "codes")
+    check(M.moe_fp8_linear(x, w, ws, out_dtype=F32)[at:], ref, tol, None, "values")
+
+
+@pytest.mark.parametrize("kind", EVERY)
+def test_largest_weight(M, kind):
+    """Just under 2^31 codes: streamed and in tiles, the last columns."""
+    n, k, at = 131071, 16368, 130816
+    w = device_codes(n, k, 4)
+    ws = scales_of(kind, n, k, 5).to(DEV)
+    for T in (3, 70):
+        assert (plan(T, n, k)[0] > 0) == (T == 70)
+        c, s, _, _ = M.moe_fp8_quantize(hidden(T, k, T).to(DEV))
+        xv, wv = values(c, s, 1), values(w[at:], ws[at:] if kind == "row" else ws[at // 128:], 1 if kind == "row" else 128)
+        y = M.moe_fp8_linear(c, w, ws, x_scales=s, out_dtype=F32)
+        check(y[:, at:], xv @ wv.T, sum_tol(xv, wv), None, f"{T} rows")
+
+
+def test_largest_weight_quantised(M):
+    n, k, at = 131071, 16368, 130944
+    w = torch.randn(n, k, dtype=BF, device=DEV, generator=torch.Generator(device=DEV).manual_seed(6))
+    c, s, ct, st = M.moe_fp8_quantize_weight(w, U8, transpose=True)
+    rc, rs, rct, rst = M.moe_fp8_quantize_weight(w[at:].clone(), U8, transpose=True)
+    assert torch.equal(c[at:], rc) and torch.equal(s[-1:], rs) and torch.equal(ct[:, at:], rct) and torch.equal(st[:, -1:], rst)
+
+
+@pytest.mark.parametrize("dt", [BF, F32])
+def test_largest_result(M, dt):
+    T, n, k, at = 32767, 65528, 16, 32700
+    x, w, ws = hidden(T, k, 7).to(DEV), device_codes(n, k, 8), scales_of("f32", n, k, 9).to(DEV)
+    c, s, _, _ = M.moe_fp8_quantize(x)
+    xv, wv = values(c[at:], s[at:], 1), values(w, ws, 128)
+    y = torch.ones(T, n, dtype=dt, device=DEV)
+    M.moe_fp8_linear(c, w, ws, x_scales=s, residual=y, out=y)
+    check(y[at:], xv @ wv.T, sum_tol(xv, wv), torch.ones(T - at, n, dtype=dt, device=DEV), "y")
+
+
+def test_most_rows(M):
+    """Rows of 8 values, as many as 2^31 values allow: the grid has nearly 2^32 threads."""
+    T, at = 2 ** 28 - 16, 2 ** 28 - 80
+    x = torch.randn(T, 8, dtype=BF, device=DEV, generator=torch.Generator(device=DEV).manual_seed(1))
+    c, s, _, _ = M.moe_fp8_quantize(x)
+    rc, rs, _, _ = M.moe_fp8_quantize(x[at:].clone())
+    assert torch.equal(c[at:], rc) and torch.equal(s[at:], rs)
+    mid = slice(2 ** 27 - 64, 2 ** 27 + 64)
+    assert torch.equal(c[mid], M.moe_fp8_quantize(x[mid].clone())[0])
+    assert torch.equal(M.moe_fp8_dequant(c, s)[at:], M.moe_fp8_dequant(rc, rs))
+    with pytest.raises(M.MoeError, match="65535 blocks"):
+        M.moe_fp8_quantize(x[:65535 * 128 + 1], cols=True)
+    w = torch.ones(8, device=DEV)
+    y = M.moe_block_norm(x, w_after=w)[0]
+    assert torch.equal(y[at:], M.moe_block_norm(x[at:].clone(), w_after=w)[0])
+    dz = M.moe_block_norm_backward(x, w_after=w, dy=y, want=("dz",))[0]
+    assert torch.equal(dz[at:], M.moe_block_norm_backward(x[at:].clone(), w_after=w, dy=y[at:].clone(), want=("dz",))[0])
