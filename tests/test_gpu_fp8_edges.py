@@ -394,3 +394,37 @@ def test_most_rows(M):
     assert torch.equal(y[at:], M.moe_block_norm(x[at:].clone(), w_after=w)[0])
     dz = M.moe_block_norm_backward(x, w_after=w, dy=y, want=("dz",))[0]
     assert torch.equal(dz[at:], M.moe_block_norm_backward(x[at:].clone(), w_after=w, dy=y[at:].clone(), want=("dz",))[0])
+
+
+# ------------------------------------------------------------------ two calls at once
+
+@pytest.mark.parametrize("T", [3, 40, 300])
+def test_experts_and_norm_gradients_on_two_streams(M, T):
+    """The same weights on two streams, a workspace and results for each: the bits of either alone."""
+    E, k, H, I = 8, 2, 1280, 256
+    w, _ = device_experts(M, E, H, I, 11)
+    wa = torch.rand(H, device=DEV) + 0.5
+    sides = []
+    for i in range(2):
+        x = hidden(T, H, 30 + i).to(DEV)
+        ids = torch.stack([torch.randperm(E, generator=torch.Generator().manual_seed(40 * i + t))[:k] for t in range(T)]).to(torch.int32).to(DEV)
+        offs, sp, _ = M.moe_permute(ids, E)
+        y, ws = torch.empty(T * k, H, device=DEV), torch.empty(M.binding.moe_expert_ffn_workspace(w, "fp8", T, k), dtype=U8, device=DEV)
+        out = (torch.empty_like(x), torch.empty_like(x), torch.empty(H, device=DEV), None, None)
+        ws2 = torch.empty(M.binding.moe_block_norm_backward_workspace(T, H), dtype=U8, device=DEV)
+
+        def run(x=x, offs=offs, sp=sp, y=y, ws=ws, out=out, ws2=ws2):
+            M.moe_expert_ffn(w, x, "fp8", k, offs, sp, out=y, ws=ws)
+            M.moe_block_norm_backward(x, w_after=wa, dy=x, want=("dz", "dresidual", "dw_after"), out=out, ws=ws2)
+            return y, *out[:3]
+        sides.append((run, [t.clone() for t in run()], (y, *out[:3])))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for s, (run, _, _) in zip(streams, sides):
+            with torch.cuda.stream(s):
+                run()
+    torch.cuda.synchronize()
+    for _, ref, got in sides:
+        for a, b in zip(ref, got):
+            assert torch.equal(a, b)
