@@ -428,3 +428,44 @@ def test_experts_and_norm_gradients_on_two_streams(M, T):
     for _, ref, got in sides:
         for a, b in zip(ref, got):
             assert torch.equal(a, b)
+
+
+# ------------------------------------------------------------------ values that are not finite
+
+@pytest.mark.parametrize("E,T", [(8, 3), (256, 60), (8, 40), (4, 700)])
+def test_non_finite_values_stay_in_their_rows(M, E, T):
+    """Few rows, streamed experts, tiles of 64 and of more rows: a NaN or infinite x spoils its token's rows, a NaN code of gate its column of its expert's
+    h (and so those rows of y), one of down its column of y; every other value keeps its bits."""
+    k, H, I = 1, 512, 4480 if T == 700 else 256
+    w, _ = device_experts(M, E, H, I, 13)
+    x = hidden(T, H, 14).to(DEV)
+    ids = (torch.arange(T, dtype=torch.int32)[:, None] % E).to(DEV)
+    offs, sp, p2r = M.moe_permute(ids, E)
+    run = lambda x: (*M.moe_expert_gateup(w, x, "fp8", k, offs, sp), M.moe_expert_ffn(w, x, "fp8", k, offs, sp))
+    if T == 700:
+        assert (3, "one") in expert_forms([175] * 4, I, True, H // 128)
+    clean = run(x)
+    assert all(torch.isfinite(t).all() for t in (clean[0], clean[3]))
+    row, e = p2r.view(-1).long(), sp.long() % E                # (a token's row; a row's expert)
+    for bad in (float("nan"), float("inf")):
+        z = x.clone()
+        z[1, 130] = bad
+        h, hq, hs, y = run(z)
+        hit = torch.zeros(T, dtype=torch.bool, device=DEV)
+        hit[row[1]] = True
+        assert torch.isnan(h[hit]).all() and ((hq[hit] & 127) == 127).all() and torch.isnan(y[hit]).all()
+        for a, b in zip((h, hq, hs, y), clean):
+            assert torch.equal(a[~hit], b[~hit])
+    hit = e == 2
+    w.gate[2, 100, 7] = 0x7F
+    h, hq, hs, y = run(x)
+    col = torch.arange(I, device=DEV) == 100
+    assert torch.isnan(h[hit][:, col]).all() and torch.isnan(y[hit]).all() and torch.equal(h[hit][:, ~col], clean[0][hit][:, ~col])
+    for a, b in zip((h, hq, hs, y), clean):
+        assert torch.equal(a[~hit], b[~hit])
+    w.gate[2, 100, 7] = 0
+    base = run(x)
+    w.down[2, 300, 9] = 0x7F
+    y = run(x)[3]
+    col = torch.arange(H, device=DEV) == 300
+    assert torch.isnan(y[hit][:, col]).all() and torch.equal(y[hit][:, ~col], base[3][hit][:, ~col]) and torch.equal(y[~hit], base[3][~hit])
